@@ -379,6 +379,148 @@ qoq_status qoq_kv4_decode_attention(const void *q_fp16, const uint8_t *k_codes, 
                                     size_t *workspace_bytes, void *stream);
 
 /*
+ * Paged KV4 cache: the same per-vector 4-bit quantiser over pages of
+ * page_size tokens, for serving steps in which every request brings its own
+ * number of new tokens (a decoding request one, a prompt or a chunk of one
+ * many, drafted tokens a few). The steps' buffers are all device memory; one
+ * set of page tables serves every layer's cache.
+ *
+ * State of the requests (rows 0 .. B - 1 of the block table)
+ *   seq_lens    int32 [B]             tokens cached so far
+ *   block_table int32 [B][max_pages]  entry i: the page of tokens
+ *                                     i * page_size .. (i + 1) * page_size - 1
+ *   free_pages  int32 [n_pages]       a stack of free page numbers, of which the
+ *   free_count  int32 [1]             first free_count entries hold
+ * and of one layer's cache, for K and for V
+ *   codes  uint8 [n_pages][Hkv][page_size][D/2], byte j = q[2j] | q[2j+1] << 4
+ *   params FP16  [n_pages][Hkv][page_size][2], scale then zero
+ * A token's slot is page * page_size + its offset in the page. page_size is
+ * 16, 32, 64, 128 or 256, n_pages * page_size at most INT32_MAX.
+ *
+ * qoq_kv4_pages_assign begins a step: new_lens int32 [B] tokens (>= 0) join
+ * each request. A request takes ceil((s + n) / P) - ceil(s / P) pages; over
+ * the batch, in request order, the k-th page taken is
+ * free_pages[free_count - 1 - k]. Written:
+ *   kv_lens   int32 [B]           seq_lens + new_lens
+ *   q_start   int32 [B + 1]       first row of each request's new tokens
+ *   positions int32 [max_tokens]  position of each row's token in its sequence
+ *   slots     int32 [max_tokens]  its cache slot
+ *   block_table                   the entries of the pages taken
+ *   free_left int32 [1]           free_count less the pages taken
+ * Rows of positions and slots from q_start[B] on are -1 (the attention and
+ * the cache calls skip them), so one captured step serves any batch up to
+ * max_tokens rows. kv_lens may be seq_lens itself and free_left free_count
+ * itself (the step in place); no other buffers may overlap.
+ * A step that does not fit is refused whole: with a negative length or a page
+ * number outside [0, n_pages) among the entries it reads (QOQ_ERR_INVALID_ARG),
+ * more than max_tokens rows, a request beyond max_pages or more pages than
+ * are free (QOQ_ERR_WORKSPACE) the state is copied unchanged, q_start is all
+ * 0 and every slot and position -1, so the step's other calls do nothing.
+ * status: int32 [4], zeroed by the caller before first use; [0] stays 0 or
+ * becomes the first refused step's code with [1] the request (-1: the whole
+ * step), [2] the rows and [3] the pages that the step wanted (each at most
+ * INT32_MAX); the caller clears it.
+ *
+ * qoq_kv4_pages_release ends requests: for each b with leave[b] != 0 (int32
+ * [B]) the pages of its seq_lens[b] tokens go back to free_pages, its entries
+ * become -1 and seq_lens[b] 0. Pages are pushed in the reverse of the order in
+ * which qoq_kv4_pages_assign would take them, so releasing what one step
+ * took restores the stack. A page number outside [0, n_pages)
+ * or a negative or too long sequence (QOQ_ERR_INVALID_ARG), or more pages than the stack has room
+ * for (QOQ_ERR_WORKSPACE), refuses the whole call: nothing changes but status.
+ * Every page belongs to one request (nothing is reference-counted).
+ *
+ * Both calls: B at most 16384 (else QOQ_ERR_UNSUPPORTED); buffers 4-byte
+ * aligned. B == 0 leaves the state as it is; assign then writes q_start[0]
+ * = 0, its rows -1 and free_left.
+ */
+qoq_status qoq_kv4_pages_assign(const int32_t *seq_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
+                                const int32_t *free_pages, const int32_t *free_count, int64_t n_pages,
+                                int32_t *block_table, int64_t max_pages, int64_t max_tokens, int32_t *kv_lens,
+                                int32_t *q_start, int32_t *positions, int32_t *slots, int32_t *free_left,
+                                int32_t *status, void *stream);
+
+qoq_status qoq_kv4_pages_release(const int32_t *leave, int64_t B, int64_t page_size, int32_t *seq_lens,
+                                 int32_t *block_table, int64_t max_pages, int32_t *free_pages, int32_t *free_count,
+                                 int64_t n_pages, int32_t *status, void *stream);
+
+/*
+ * Paged cache write and read (layout above, arithmetic of
+ * qoq_kv4_cache_write, bit for bit).
+ *
+ * qoq_kv4_paged_write quantises rows 0 .. N - 1 of k and v, FP16 [N][Hkv][D]
+ * with row strides of k_stride and v_stride elements (the heads of a row are
+ * dense; views of a merged projection's output need no copy), into
+ * slots[row]. qoq_kv4_paged_read gathers the same slots back: k_out and v_out
+ * FP16 [N][Hkv][D] (dense) = FP16((q - z) * s), one rounding. Rows whose slot lies
+ * outside [0, n_pages * page_size) are not written, and read as 0. The slots
+ * of one write must differ from one another (those outside the range need
+ * not).
+ *
+ * D 64 or 128; strides multiples of 8 and at least Hkv * D; k, v, codes and
+ * outputs 16-byte aligned, params and slots 4-byte. N == 0 is a no-op.
+ */
+qoq_status qoq_kv4_paged_write(const void *k_fp16, int64_t k_stride, const void *v_fp16, int64_t v_stride,
+                               const int32_t *slots, int64_t N, int64_t Hkv, int64_t D, int64_t n_pages,
+                               int64_t page_size, uint8_t *k_codes, void *k_params, uint8_t *v_codes,
+                               void *v_params, void *stream);
+
+qoq_status qoq_kv4_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int64_t D, int64_t n_pages,
+                              int64_t page_size, const uint8_t *k_codes, const void *k_params,
+                              const uint8_t *v_codes, const void *v_params, void *k_out_fp16, void *v_out_fp16,
+                              void *stream);
+
+/*
+ * Attention of new tokens over a paged KV4 cache: a ragged batch of requests,
+ * request b with rows q_start[b] .. q_start[b + 1] - 1 of q (n_b of them) and
+ * kv_lens[b] cached tokens, its new ones (already written) among them. One
+ * row per request is a decode step, many are a prompt, a chunk of one, or
+ * drafted tokens; a batch may mix them.
+ *
+ *   row i of request b stands at position p = kv_lens[b] - n_b + i and sees
+ *   token t of its request when t <= p and, with window > 0, also
+ *   p - t < window or t < sinks (a sliding window over the latest tokens, the
+ *   row's own among them, and the first `sinks` tokens, which stay visible);
+ *   score_t = (q . k_t) / sqrt(D);  out = sum_t softmax_t(score) v_t
+ *   with k_t, v_t = (q_t - z_t) * s_t, query head hq on KV head
+ *   hq / (Hq / Hkv). A row that sees no token (p < 0) gives zeros.
+ *
+ * q FP16 [N][Hq][D] with a row stride of q_stride elements; out FP16
+ * [N][Hq][D] with out_stride. Rows that belong to no request are left as they
+ * are. Scores, softmax and outputs are kept in FP32; the softmax weights
+ * times the value scales are rounded to FP16 for the product with the value
+ * codes, and the output is rounded once, so |o - o*| <= 2^-10 max|v| + 2^-24
+ * per row and head, with max|v| over the request's visible tokens. The cached
+ * values of the tokens that no row sees do not matter, whatever they hold.
+ *
+ * max_new: an upper bound of n_b known on the host (1 for a decode step); it
+ * selects the kernels. kv_lens and q_start are clamped to what the buffers
+ * hold. A request with n_b > max_new, or whose visible tokens lie on a page
+ * outside [0, n_pages), sets the status word to QOQ_ERR_INVALID_ARG: the
+ * former's rows are left as they are, the latter's tokens on such pages count
+ * as k = v = 0.
+ *
+ * Hq a multiple of Hkv with Hq / Hkv <= 8, D 64 or 128; strides multiples of
+ * 8 and at least Hq * D; window >= 0 (0: none), sinks >= 0 (no effect without
+ * a window); q, codes and out 16-byte aligned, the rest 4-byte.
+ * B at most 16384, Hkv at most 65535. N == 0 or B == 0 is a no-op.
+ *
+ * Workspace: as for qoq_kv4_decode_attention: size query with workspace ==
+ * NULL, 256-byte aligned, zero-filled before its first use, status words in
+ * bytes [0, 256) ([0] the code; with QOQ_ERR_INVALID_ARG [1] = the request),
+ * control words that every call leaves zero, then scratch; calls that may
+ * overlap on the device need separate workspaces. The size depends on B, N,
+ * the heads and max_new, not on the lengths.
+ */
+qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const uint8_t *k_codes,
+                                   const void *k_params, const uint8_t *v_codes, const void *v_params,
+                                   const int32_t *block_table, int64_t max_pages, const int32_t *q_start,
+                                   const int32_t *kv_lens, int64_t B, int64_t N, int64_t max_new, int64_t Hq,
+                                   int64_t Hkv, int64_t D, int64_t n_pages, int64_t page_size, int64_t window,
+                                   int64_t sinks, void *out_fp16, int64_t out_stride, void *workspace,
+                                   size_t *workspace_bytes, void *stream);
+
+/*
  * Launch plan of a problem (no device work; the library has no counterpart
  * in the QServe pages): the token tile (MMA N: 16, 32, 64, 128 or 256) the
  * GEMM calls use for (M, N, K), and how many kernels qoq_w4a8_linear

@@ -26,3 +26,4 @@ from a printed value.
 from .qoq_ref import *  # noqa: F401,F403
 from . import producers  # noqa: F401
 from . import kv4  # noqa: F401
+from . import kv4_paged  # noqa: F401

@@ -1,0 +1,31 @@
+// What the paged KV4 attention kernels share: their arguments, and a
+// request's rows and tokens from the device-side lengths.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "qoq_device.cuh"
+#include "qoq_internal.h"
+
+namespace qoq {
+
+// A request's rows of q and out, and its cached tokens, clamped to what the
+// buffers hold whatever the device arrays say.
+struct PagedRequest {
+    int row0, n, kv;
+};
+
+__device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams &p, int b) {
+    PagedRequest r;
+    r.row0 = min(max(p.q_start[b], 0), (int)p.N);
+    r.n = max(min(p.q_start[b + 1], (int)p.N) - r.row0, 0);
+    r.kv = (int)min((int64_t)max(p.kv_lens[b], 0), (int64_t)p.max_pages << p.page_shift);
+    return r;
+}
+
+__device__ __forceinline__ void paged_bad_request(const PagedAttnParams &p, int b) {
+    if (atomicCAS(p.status, 0, QOQ_ERR_INVALID_ARG) == 0) p.status[1] = b;
+}
+
+}  // namespace qoq

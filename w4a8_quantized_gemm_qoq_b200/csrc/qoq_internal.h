@@ -1,6 +1,7 @@
 // Host-side declarations shared by the library's translation units.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -153,6 +154,41 @@ size_t kv4_workspace_bytes(int64_t B, int64_t Hkv, int64_t Tmax, int64_t D);
 cudaError_t launch_kv4_attention(const void *q, const uint8_t *kc, const void *ks, const void *kz, const uint8_t *vc,
                                  const void *vs, const void *vz, const int32_t *seq_lens, int64_t B, int64_t Hq,
                                  int64_t Hkv, int64_t Tmax, int64_t D, void *out, void *ws, cudaStream_t stream);
+
+// Paged KV4 cache: page tables (kv4_pages.cu), write and read
+// (kv4_paged_cache.cu), attention (kv4_paged_attention.cu).
+cudaError_t launch_pages_assign(const int32_t *seq_lens, const int32_t *new_lens, int64_t B, int page_shift,
+                                const int32_t *free_pages, const int32_t *free_count, int64_t n_pages,
+                                int32_t *block_table, int64_t max_pages, int64_t max_tokens, int32_t *kv_lens,
+                                int32_t *q_start, int32_t *positions, int32_t *slots, int32_t *free_left,
+                                int32_t *status, cudaStream_t stream);
+cudaError_t launch_pages_release(const int32_t *leave, int64_t B, int page_shift, int32_t *seq_lens,
+                                 int32_t *block_table, int64_t max_pages, int32_t *free_pages, int32_t *free_count,
+                                 int64_t n_pages, int32_t *status, cudaStream_t stream);
+cudaError_t launch_paged_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int32_t *slots,
+                               int64_t N, int64_t Hkv, int64_t D, int64_t n_pages, int page_shift, uint8_t *k_codes,
+                               void *k_params, uint8_t *v_codes, void *v_params, cudaStream_t stream);
+cudaError_t launch_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int64_t D, int64_t n_pages, int page_shift,
+                              const uint8_t *k_codes, const void *k_params, const uint8_t *v_codes,
+                              const void *v_params, void *k_out, void *v_out, cudaStream_t stream);
+
+constexpr int kMaxPagedBatch = 16384;   // requests per paged step
+
+struct PagedAttnParams {
+    const __half *q;
+    int64_t q_stride;
+    const uint8_t *k_codes, *v_codes;
+    const __half2 *k_params, *v_params;   // (scale, zero)
+    const int32_t *block_table, *q_start, *kv_lens;
+    __half *out;
+    int64_t out_stride;
+    int32_t *status;     // workspace: [0] code, [1] request
+    int64_t N;
+    int B, max_pages, max_new, Hq, Hkv, G, n_pages, page_shift, window, sinks;
+    float qscale;        // log2(e) / sqrt(D)
+};
+size_t kv4_paged_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_new);
+cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, cudaStream_t stream);
 
 // Row width limit of the fused producers (the row lives in registers: at most
 // 8 chunks of 8 elements per thread of a 512-thread row, or 4 of a 1024-thread row).

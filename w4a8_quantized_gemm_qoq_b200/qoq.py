@@ -7,6 +7,7 @@ raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -53,6 +54,15 @@ def lib() -> ctypes.CDLL:
         L.qoq_kv4_cache_write.restype = ctypes.c_int
         L.qoq_kv4_decode_attention.argtypes = [vp] * 8 + [i64] * 5 + [vp, vp, sz, vp]
         L.qoq_kv4_decode_attention.restype = ctypes.c_int
+        L.qoq_kv4_pages_assign.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, i64, i64] + [vp] * 7
+        L.qoq_kv4_pages_release.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp]
+        L.qoq_kv4_paged_write.argtypes = [vp, i64, vp, i64, vp] + [i64] * 5 + [vp] * 5
+        L.qoq_kv4_paged_read.argtypes = [vp] + [i64] * 5 + [vp] * 7
+        L.qoq_kv4_paged_attention.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, vp, vp] + [i64] * 10 + \
+            [vp, i64, vp, sz, vp]
+        for f in (L.qoq_kv4_pages_assign, L.qoq_kv4_pages_release, L.qoq_kv4_paged_write, L.qoq_kv4_paged_read,
+                  L.qoq_kv4_paged_attention):
+            f.restype = ctypes.c_int
         L.qoq_plan.argtypes = [i64, i64, i64, vp, vp]
         L.qoq_plan.restype = ctypes.c_int
         L.qoq_watchdog_selftest.argtypes = [vp, i64, vp]
@@ -334,4 +344,241 @@ def kv4_decode_attention(q, kcache, vcache, seq_lens=None, ws=None, out=None, st
         _ptr(q), _ptr(kcache.codes), _ptr(kcache.scales), _ptr(kcache.zeros), _ptr(vcache.codes),
         _ptr(vcache.scales), _ptr(vcache.zeros), _ptr(seq_lens), B, Hq, kcache.Hkv, kcache.T, D, _ptr(out),
         _ptr(ws.buf), ctypes.byref(n), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ paged KV4
+
+def _device_scope(t):
+    """Launches go to the device of the tensors: a no-op when it is current."""
+    import torch
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _i32_buffer(t, shape, like, name):
+    """An int32 CUDA tensor of this shape on the device of `like`."""
+    import torch
+    t = _cuda_tensor(t, torch.int32, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, like.device))
+    return t
+
+
+def _rows(t, name, D=None):
+    """FP16 [N][heads][D] with dense heads and any row stride; returns the row
+    stride in elements."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.float16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.float16, t.dtype))
+    if t.dim() != 3 or (D is not None and t.shape[2] != D):
+        raise ValueError("%s must have shape [N][heads][%s]" % (name, "D" if D is None else D))
+    n, h, d = t.shape
+    if n and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError("the heads of a row of %s must be dense" % name)
+    return t.stride(0) if n > 1 else h * d
+
+
+class PagedStep:
+    """What one step of up to max_tokens rows needs of the page tables
+    (include/qoq.h, qoq_kv4_pages_assign): q_start [B + 1], and positions and
+    slots [max_tokens], -1 past the step's rows."""
+
+    def __init__(self, B, max_tokens, device="cuda"):
+        import torch
+        self.q_start = torch.zeros((B + 1,), dtype=torch.int32, device=device)
+        self.positions = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
+        self.slots = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
+
+
+class PageTable:
+    """Pages of B requests, kept on the GPU: cached lengths, block table, and
+    the stack of free pages (include/qoq.h, "Paged KV4 cache"). One table
+    serves the caches of every layer."""
+
+    def __init__(self, B, max_pages, n_pages, page_size=64, device="cuda"):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        self._set(torch.zeros((B,), **i32), torch.full((B, max_pages), -1, **i32), torch.arange(n_pages, **i32),
+                  torch.full((1,), n_pages, **i32), page_size)
+
+    @classmethod
+    def of(cls, seq_lens, block_table, free_pages, free_count, page_size):
+        """A table over buffers the caller already holds (not copied)."""
+        self = cls.__new__(cls)
+        self._set(seq_lens, block_table, free_pages, free_count, page_size)
+        return self
+
+    def _set(self, seq_lens, block_table, free_pages, free_count, page_size):
+        import torch
+        self.seq_lens = _cuda_tensor(seq_lens, torch.int32, "seq_lens")
+        if seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("seq_lens [B], block_table [B][max_pages] and free_pages [n_pages] are expected")
+        self.B = seq_lens.shape[0]
+        self.block_table = _i32_buffer(block_table, (self.B, block_table.shape[1]), seq_lens, "block_table")
+        self.free_pages = _i32_buffer(free_pages, free_pages.shape, seq_lens, "free_pages")
+        self.free_count = _i32_buffer(free_count, (1,), seq_lens, "free_count")
+        self.page_size = int(page_size)
+        self.status_words = torch.zeros((4,), dtype=torch.int32, device=seq_lens.device)
+
+    def assign(self, new_lens, step, kv_lens=None, free_left=None, stream=None):
+        """Begin a step in which new_lens[b] tokens join request b: fills
+        `step` and enters the pages taken. The lengths and the free count
+        are updated in place, unless kv_lens [B] and free_left [1] are given
+        to take the new ones. Returns `step`."""
+        s = self.seq_lens
+        new_lens = _i32_buffer(new_lens, (self.B,), s, "new_lens")
+        _i32_buffer(step.q_start, (self.B + 1,), s, "step.q_start")
+        n = step.slots.shape[0]
+        kv_lens = s if kv_lens is None else _i32_buffer(kv_lens, (self.B,), s, "kv_lens")
+        free_left = self.free_count if free_left is None else _i32_buffer(free_left, (1,), s, "free_left")
+        with _device_scope(s):
+            _check("qoq_kv4_pages_assign", lib().qoq_kv4_pages_assign(
+                _ptr(s), _ptr(new_lens), self.B, self.page_size, _ptr(self.free_pages), _ptr(self.free_count),
+                self.free_pages.shape[0], _ptr(self.block_table), self.block_table.shape[1], n, _ptr(kv_lens),
+                _ptr(step.q_start), _ptr(step.positions), _ptr(step.slots), _ptr(free_left), _ptr(self.status_words),
+                _stream(stream)))
+        return step
+
+    def release(self, leave, stream=None):
+        """End the requests b with leave[b] != 0 (int32 [B]): their pages are
+        free again, their lengths 0."""
+        s = self.seq_lens
+        leave = _i32_buffer(leave, (self.B,), s, "leave")
+        with _device_scope(s):
+            _check("qoq_kv4_pages_release", lib().qoq_kv4_pages_release(
+                _ptr(leave), self.B, self.page_size, _ptr(s), _ptr(self.block_table), self.block_table.shape[1],
+                _ptr(self.free_pages), _ptr(self.free_count), self.free_pages.shape[0], _ptr(self.status_words),
+                _stream(stream)))
+
+    def status(self) -> int:
+        """The first refused step's status code (synchronises), 0 if none was."""
+        return int(self.status_words[0].item())
+
+
+class PagedKV4Cache:
+    """One layer's paged 4-bit cache of K and V (include/qoq.h, "Paged KV4
+    cache"): codes uint8 [n_pages][Hkv][page_size][D/2] and params FP16
+    [n_pages][Hkv][page_size][2] (scale, zero) of each."""
+
+    def __init__(self, n_pages, Hkv, page_size, D, device="cuda"):
+        import torch
+        u8 = dict(dtype=torch.uint8, device=device)
+        f16 = dict(dtype=torch.float16, device=device)
+        self._set(torch.zeros((n_pages, Hkv, page_size, D // 2), **u8),
+                  torch.zeros((n_pages, Hkv, page_size, 2), **f16),
+                  torch.zeros((n_pages, Hkv, page_size, D // 2), **u8),
+                  torch.zeros((n_pages, Hkv, page_size, 2), **f16))
+
+    @classmethod
+    def of(cls, k_codes, k_params, v_codes, v_params):
+        """A cache over buffers the caller already holds (not copied)."""
+        self = cls.__new__(cls)
+        self._set(k_codes, k_params, v_codes, v_params)
+        return self
+
+    def _set(self, k_codes, k_params, v_codes, v_params):
+        import torch
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _cuda_tensor(t, torch.uint8, name)
+        for t, name in ((k_params, "k_params"), (v_params, "v_params")):
+            _cuda_tensor(t, torch.float16, name)
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must have shape [n_pages][Hkv][page_size][D/2]")
+        n, h, P, db = k_codes.shape
+        if tuple(v_codes.shape) != (n, h, P, db) or tuple(k_params.shape) != (n, h, P, 2) or \
+                tuple(v_params.shape) != (n, h, P, 2):
+            raise ValueError("the shapes of codes and params do not match")
+        if len({t.device for t in (k_codes, k_params, v_codes, v_params)}) != 1:
+            raise ValueError("codes and params must be on one device")
+        self.n_pages, self.Hkv, self.page_size, self.D = n, h, P, 2 * db
+        self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
+        self._ptrs = tuple(_ptr(t) for t in (k_codes, k_params, v_codes, v_params))
+
+    def write(self, k, v, slots, stream=None):
+        """Quantise rows k, v [N][Hkv][D] FP16 (any row stride) into
+        slots [N] int32; rows with a slot outside the cache are skipped."""
+        ks, vs = _rows(k, "k", self.D), _rows(v, "v", self.D)
+        N = k.shape[0]
+        if k.shape[1] != self.Hkv or v.shape != k.shape:
+            raise ValueError("k %s and v %s do not match the cache" % (tuple(k.shape), tuple(v.shape)))
+        slots = _i32_buffer(slots, (N,), self.k_codes, "slots")
+        if k.device != slots.device or v.device != slots.device:
+            raise ValueError("k and v must be on the cache's device")
+        with _device_scope(self.k_codes):
+            _check("qoq_kv4_paged_write", lib().qoq_kv4_paged_write(
+                _ptr(k), ks, _ptr(v), vs, _ptr(slots), N, self.Hkv, self.D, self.n_pages, self.page_size,
+                *self._ptrs, _stream(stream)))
+        return self
+
+    def read(self, slots, k=None, v=None, stream=None):
+        """The cached K and V of slots [N] as FP16 [N][Hkv][D] each (a sequence
+        moved elsewhere, or handed to a dense kernel); 0 outside the cache."""
+        import torch
+        slots = _i32_buffer(slots, (slots.shape[0],), self.k_codes, "slots")
+        shape = (slots.shape[0], self.Hkv, self.D)
+        with _device_scope(self.k_codes):
+            with _stream_scope(stream):
+                k = torch.empty(shape, dtype=torch.float16, device=slots.device) if k is None else k
+                v = torch.empty(shape, dtype=torch.float16, device=slots.device) if v is None else v
+            for t, name in ((k, "k"), (v, "v")):
+                _cuda_tensor(t, torch.float16, name)
+                if tuple(t.shape) != shape or t.device != slots.device:
+                    raise ValueError("%s must have shape %s on %s" % (name, shape, slots.device))
+            _check("qoq_kv4_paged_read", lib().qoq_kv4_paged_read(
+                _ptr(slots), shape[0], self.Hkv, self.D, self.n_pages, self.page_size, *self._ptrs, _ptr(k), _ptr(v),
+                _stream(stream)))
+        return k, v
+
+
+def _stream_scope(stream):
+    """Allocations belong to the stream that uses them."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def kv4_paged_workspace_bytes(B, N, Hq, Hkv, D, max_new) -> int:
+    n = ctypes.c_size_t(0)
+    _check("qoq_kv4_paged_attention", lib().qoq_kv4_paged_attention(
+        None, 0, None, None, None, None, None, 0, None, None, B, N, max_new, Hq, Hkv, D, 0, 0, 0, 0, None, 0, None,
+        ctypes.byref(n), None))
+    return n.value
+
+
+def kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window=0, sinks=0, ws=None, out=None,
+                        stream=None):
+    """q [N][Hq][D] FP16 (any row stride): rows q_start[b] .. q_start[b + 1] - 1
+    are request b's latest tokens, attending to the kv_lens[b] tokens that
+    block_table [B][max_pages] holds of it, causally, and with window > 0 only
+    to the latest `window` of them and the first `sinks`. max_new bounds the rows per request (1 for a decode
+    step). Returns out [N][Hq][D] FP16."""
+    import torch
+    qs = _rows(q, "q", cache.D)
+    N, Hq, D = q.shape
+    like = cache.k_codes
+    B = block_table.shape[0]
+    _i32_buffer(block_table, (B, block_table.shape[1]), like, "block_table")
+    _i32_buffer(q_start, (B + 1,), like, "q_start")
+    _i32_buffer(kv_lens, (B,), like, "kv_lens")
+    if q.device != like.device:
+        raise ValueError("q is on %s, not on %s" % (q.device, like.device))
+    with _device_scope(like):
+        with _stream_scope(stream):
+            if ws is None:
+                ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, D, max_new), q.device)
+            if out is None:
+                out = torch.empty((N, Hq, D), dtype=torch.float16, device=q.device)
+        os_ = _rows(out, "out", D)
+        if out.shape != q.shape or out.device != q.device or ws.buf.device != q.device:
+            raise ValueError("out must have q's shape, out and ws its device")
+        n = ctypes.c_size_t(ws.buf.numel())
+        _check("qoq_kv4_paged_attention", lib().qoq_kv4_paged_attention(
+            _ptr(q), qs, *cache._ptrs, _ptr(block_table), block_table.shape[1], _ptr(q_start), _ptr(kv_lens), B, N,
+            max_new, Hq, cache.Hkv, D, cache.n_pages, cache.page_size, window, sinks, _ptr(out), os_, _ptr(ws.buf),
+            ctypes.byref(n), _stream(stream)))
     return out
