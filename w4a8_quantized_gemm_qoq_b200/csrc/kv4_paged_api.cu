@@ -183,7 +183,7 @@ qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const u
     p.window = window >= reach ? 0 : (int)window;
     p.sinks = (int)(sinks < reach ? sinks : reach);
     p.qscale = (float)(1.4426950408889634 / std::sqrt((double)D));
-    return status_of(launch_paged_attention(p, D, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_paged_attention(p, D, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -35,11 +35,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_paged_plain_kernel(const __gr
     }
     const int b = lo;
     const PagedRequest r = paged_request(p, b);
-    if (row < r.row0 || row >= r.row0 + r.n) return;
-    if (r.n > p.max_new) {
-        if (lane == 0) paged_bad_request(p, b);
-        return;
-    }
+    if (row < r.row0 || row >= r.row0 + r.n || r.n > p.max_new || r.n * p.G <= kRowsMax) return;
     const int pos = r.kv - r.n + (row - r.row0);
     for (int d = lane; d < D; d += 32) qs[warp][d] = __half2float(p.q[row * p.q_stride + hq * D + d]);
     __syncwarp();
@@ -96,9 +92,14 @@ __global__ void __launch_bounds__(32 * kWarps) kv4_paged_plain_kernel(const __gr
 
 }  // namespace
 
-size_t kv4_paged_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 256; }
+// Bytes [0, 256) are the status words; the few-rows kernel's part follows.
+size_t kv4_paged_workspace_bytes(int64_t B, int64_t, int64_t, int64_t, int64_t D, int64_t) {
+    return 256 + rows_workspace_bytes(B, D);
+}
 
-cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, void *ws, cudaStream_t stream) {
+    const cudaError_t e = launch_paged_rows(p, D, static_cast<uint8_t *>(ws) + 256, stream);
+    if (e != cudaSuccess || (int64_t)p.max_new * p.G <= kRowsMax) return e;
     const unsigned blocks = (unsigned)((p.N * p.Hq + kWarps - 1) / kWarps);
     if (D == 128)
         kv4_paged_plain_kernel<128><<<blocks, 32 * kWarps, 0, stream>>>(p);
