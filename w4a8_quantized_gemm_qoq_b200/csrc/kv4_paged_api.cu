@@ -138,6 +138,7 @@ qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const u
     if (st != QOQ_OK) return st;
     if (Hq <= 0 || B < 0 || N < 0 || max_new < 1) return QOQ_ERR_INVALID_ARG;
     if (Hq % Hkv != 0 || Hq / Hkv > 8 || B > kMaxPagedBatch || N > INT32_MAX / 8) return QOQ_ERR_UNSUPPORTED;
+    if (max_new > N) max_new = N > 0 ? N : 1;
     const size_t need = kv4_paged_workspace_bytes(B, N, Hq, Hkv, D, max_new);
     if (workspace == nullptr) {
         *workspace_bytes = need;
@@ -172,7 +173,7 @@ qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const u
     p.N = N;
     p.B = (int)B;
     p.max_pages = (int)max_pages;
-    p.max_new = (int)(max_new < N ? max_new : N);
+    p.max_new = (int)max_new;
     p.Hq = (int)Hq;
     p.Hkv = (int)Hkv;
     p.G = (int)(Hq / Hkv);
@@ -183,7 +184,7 @@ qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const u
     p.window = window >= reach ? 0 : (int)window;
     p.sinks = (int)(sinks < reach ? sinks : reach);
     p.qscale = (float)(1.4426950408889634 / std::sqrt((double)D));
-    return status_of(launch_paged_attention(p, D, workspace, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_paged_attention(p, D, max_new, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -190,8 +190,12 @@ struct PagedAttnParams {
 constexpr int kRowsMax = 8;   // rows x heads per KV head of the few-rows kernel (columns of its products)
 size_t rows_workspace_bytes(int64_t B, int64_t D);
 cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cudaStream_t stream);
+size_t chunk_workspace_bytes(int64_t B, int64_t max_new, int64_t G, int64_t D);
+cudaError_t launch_paged_chunk(const PagedAttnParams &p, int64_t D, int rows_limit, int64_t max_new, void *ws,
+                               cudaStream_t stream);
 size_t kv4_paged_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_new);
-cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, void *ws, cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws,
+                                   cudaStream_t stream);
 
 // Row width limit of the fused producers (the row lives in registers: at most
 // 8 chunks of 8 elements per thread of a 512-thread row, or 4 of a 1024-thread row).
