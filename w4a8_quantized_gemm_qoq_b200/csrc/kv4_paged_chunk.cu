@@ -11,8 +11,8 @@
 // exactly, so the only rounding before the output is that of P. Scales are per
 // token: s_K multiplies columns of S, s_V columns of P.
 //
-// One warpgroup unpacks codes for both row tiles (each code is unpacked once
-// per 256 rows; c | 0x6400 is the half 1024 + c and c << 4 | 0x5400 is 64 + c,
+// Two warpgroups unpack the codes of K and V for both row tiles (each code is
+// unpacked once per 256 rows; c | 0x6400 is the half 1024 + c and c << 4 | 0x5400 is 64 + c,
 // so an AND-OR and a subtraction of 1024 + z or 64 + z give two codes), one
 // thread issues the products, two warpgroups do the softmaxes, in turn with
 // one another: while one row tile's softmax runs, the tensor core works on the
@@ -44,9 +44,12 @@ namespace {
 constexpr int kChCtas = 148;         // one per SM
 constexpr int kChKeys = 128;         // keys per step
 constexpr int kChRows = 256;         // rows per item: two tiles of 128
-constexpr int kChThreads = 512;      // softmax 0, softmax 1, unpack, issue (one warp of four)
+constexpr int kChThreads = 640;      // warpgroups: softmax 0 and 1, unpack K, unpack V, issue (one of its warps)
 constexpr int kChSlots = 2 * kChCtas;   // pieces of divided items
 constexpr int kChOverhead = 3;       // cost of a piece beside its steps, in steps
+// Registers per thread: the pool is 640 threads x 96, of which the roles take
+// 256 x 128 + 256 x 88 + 128 x 40 = 60416 of 61440.
+constexpr int kRegsSoftmax = 128, kRegsUnpack = 88, kRegsIssue = 40;
 constexpr float kChSlack = 6.0f;     // log2 by which scores may exceed the running maximum
 constexpr int kDvThreads = 1024;
 
@@ -196,20 +199,64 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D (+)= A . B over 64 of the inner index, both operands in shared memory with
+// that index contiguous: four products of 16, 32 bytes apart in a swizzled row.
+__device__ __forceinline__ void mma4_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %3, 1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %3, 1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %9, %10, %3, 1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "l"(a + 2ull), "l"(b + 2ull), "l"(a + 4ull), "l"(b + 4ull),
+        "l"(a + 6ull), "l"(b + 6ull)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D (+)= A . B over 64 keys: A in tensor memory (8 columns per 16 keys), B
+// with its N index contiguous (2048 bytes per 16 keys).
+__device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %3, 1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %3, 1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %3, 1;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(a + 8u), "l"(b + 128ull), "r"(a + 16u), "l"(b + 256ull),
+        "r"(a + 24u), "l"(b + 384ull)
         : "memory");
+}
+
+// Two FP32 values in one register pair, each operation on both.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    return pair_of(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 of_pair(uint64_t v) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Shared-memory descriptor of an operand whose M or N index is contiguous:
@@ -225,27 +272,77 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// Loads of 16 lanes x 32 columns in the layout of matrix fragments: lane t's
+// registers 4 j .. 4 j + 3 are row t / 4, columns 8 j + 2 (t % 4) and the next
+// one, and the same of row t / 4 + 8. Without the wait: tmem_wait16 must come
+// before any use of r.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
     __syncwarp();   // warp-collective (.sync.aligned)
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Waits for this thread's loads; the registers pass through it, so that no
+// use of them is scheduled before.
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :);
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+
+// The store that matches tmem_ld_frag, without its wait.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[16]) {
+    __syncwarp();   // warp-collective (.sync.aligned)
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+// 16 lanes x 16 columns of FP16 pairs: register 2 j is row t / 4, column 4 j + t % 4,
+// register 2 j + 1 the same of row t / 4 + 8. Without the wait.
+__device__ __forceinline__ void tmem_st_half_frag(uint32_t taddr, const uint32_t (&r)[8]) {
+    __syncwarp();   // warp-collective (.sync.aligned)
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// The load that matches tmem_st_half_frag, with its wait.
+__device__ __forceinline__ void tmem_ld_half_frag_wait(uint32_t taddr, uint32_t (&r)[8]) {
+    __syncwarp();   // warp-collective (.sync.aligned)
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ uint64_t lds64(uint32_t a) {
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void sts32f(uint32_t a, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// sts128 at a constant offset.
+template <int kOffset>
+__device__ __forceinline__ void sts128_at(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0+%5], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w), "n"(kOffset)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -253,22 +350,23 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     return half2_bits(r);
 }
 
+template <int N>
+struct Index {
+    static constexpr int value = N;
+};
+
 // ------------------------------------------------------------ shared memory
 
 template <int D>
 struct ChunkSmem {
-    static constexpr int DB = D / 2;
     static constexpr int kPanel = kChKeys * 128;            // 64 dims of 128 tokens (or rows), FP16
     static constexpr int kTile = (D / 64) * kPanel;         // one Q, K or V tile
-    static constexpr int kCodes = kChKeys * DB;             // one tile's codes
-    static constexpr int kRing = 3;                         // code tiles in flight
     static constexpr int kQ = 0;                            // two tiles
     static constexpr int kK = kQ + 2 * kTile;               // two stages
     static constexpr int kV = kK + 2 * kTile;               // two stages
-    static constexpr int kC = kV + 2 * kTile;               // code ring
-    static constexpr int kF = kC + kRing * kCodes;          // token factors: 4 x (128 K, 128 V) floats
-    static constexpr int kZ = kF + 4 * 2 * kChKeys * 4;     // zeros of the tile in work: 128 K, 128 V words
-    static constexpr int kEnd = kZ + 2 * kChKeys * 4;
+    static constexpr int kF = kV + 2 * kTile;               // token factors: 4 x (128 K, 128 V) floats
+    static constexpr int kZ = kF + 4 * 2 * kChKeys * 4;     // zeros: 2 x (128 K, 128 V) words
+    static constexpr int kEnd = kZ + 2 * 2 * kChKeys * 4;
     static constexpr int kBytes = kEnd + 1024;              // the base is rounded up to 1024
 };
 
@@ -286,10 +384,201 @@ enum ChunkSite : int {
     kSiteChunkFree = 26,    // unpacking, waiting for a free stage
 };
 
+// wait_bounded for a role that waits for long beside busy warps: each try
+// suspends the thread for up to 20 us instead of polling, which would take the
+// others' issue slots.
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, const Watchdog &wd, int site, int detail) {
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if ((it & 31u) == 31u) {
+            if (wd.aborted()) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                wd.fail(QOQ_ERR_TIMEOUT, site, detail);
+                return false;
+            }
+        }
+    }
+}
+
 // wait_bounded with one answer for the warp.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Watchdog &wd, int site, int detail) {
     const bool ok = wait_bounded(bar, parity, wd, site, detail);
     return __all_sync(0xffffffffu, ok);
+}
+
+// The softmax state of a warp's 32 rows. A thread holds four rows (8 i +
+// lane / 4 of the warp's) and of each the keys 8 j + 2 (lane % 4) and the
+// next one, so that a key's factors are read for 8 lanes and used for four
+// rows each (reading them for one row per thread would take 2048 cycles of the
+// shared memory per step).
+struct RowState {
+    float m[4];       // running maximum, in log2 units
+    uint64_t l[4];    // two partial sums over this thread's keys
+    float f[4];       // what the output so far has to be multiplied by in this step
+    uint32_t fresh;   // rows that have seen no key yet, a bit each
+};
+
+// A block of 32 keys and 32 rows: the scores x = S s_K c - m, as pairs of keys
+// [row half][4 groups of 8 keys x 2 rows], and the largest of each row's.
+struct ScoreBlock {
+    uint64_t x[2][8];
+    float top[2][2];
+};
+
+// Scores of block q, whose first 16 rows' S is on its way in raw[0]; starts the
+// load of the next block's. kf: shared-memory address of the lane's first factor.
+__device__ __forceinline__ void block_scores(uint32_t ts, uint32_t kf, int q, const RowState &st, uint32_t (&raw)[2][16],
+                                             ScoreBlock &b) {
+    uint64_t f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = lds64(kf + 128 * q + 32 * j);
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        uint32_t(&r)[16] = raw[hh];
+        tmem_wait16(r);
+        if (hh == 0) tmem_ld_frag(ts + (1u << 20) + 32u * q, raw[1]);
+        else tmem_ld_frag(ts + 32u * ((q + 1) & 3), raw[0]);   // after the last block not used
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * hh + e;
+            const uint64_t minus_m = pair_of(-st.m[i], -st.m[i]);
+            float t = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                b.x[hh][2 * j + e] = fma2(pair_of(r[4 * j + 2 * e], r[4 * j + 2 * e + 1]), f[j], minus_m);
+                const float2 y = of_pair(b.x[hh][2 * j + e]);
+                t = fmaxf(t, fmaxf(y.x, y.y));
+            }
+            b.top[hh][e] = t;
+        }
+    }
+}
+
+// p = 2^x added to the sums, P = p s_V 2^(8 - E) as FP16 over the scores' place.
+__device__ __forceinline__ void block_weights(uint32_t ts, uint32_t vf, int q, RowState &st, const ScoreBlock &b) {
+    uint64_t g[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[j] = lds64(vf + 128 * q + 32 * j);
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 y = of_pair(b.x[hh][2 * j + e]);
+                const uint64_t p = pair_of(ex2_approx(y.x), ex2_approx(y.y));
+                st.l[2 * hh + e] = add2(st.l[2 * hh + e], p);
+                const float2 z = of_pair(mul2(p, g[j]));
+                pk[2 * j + e] = half2_bits(__floats2half2_rn(z.x, z.y));
+            }
+        tmem_st_half_frag(ts + ((uint32_t)hh << 20) + 16u * q, pk);
+    }
+}
+
+__device__ __forceinline__ bool block_raises(const RowState &st, const ScoreBlock &b) {
+    return __any_sync(0xffffffffu, st.fresh != 0 || fmaxf(fmaxf(b.top[0][0], b.top[0][1]), fmaxf(b.top[1][0], b.top[1][1])) > kChSlack);
+}
+
+// A step's weights. Most steps are seen whole by every row and raise no
+// maximum, and their loop is kept to what such steps need: with the rest inside,
+// jumps over it left the instruction cache, which cost as much as the arithmetic
+// (5000 cycles a step for what takes 2400 alone). The first block that raises a
+// maximum, and a masked step, go to the loop below.
+//
+// A row's maximum is raised only when a score exceeds it by 2^kChSlack, by a
+// whole number, so that what is already stored is rescaled exactly; a row takes
+// its first maximum as it is. Key k, counted from the lane's first one, which
+// stands at position `first`, is hidden from row i where first + k > pos[i], or
+// beyond the window (pos[i] - first - k >= reach) and the sinks
+// (first + k >= sinks).
+__device__ __forceinline__ void softmax_rows(uint32_t ts, uint32_t kf, uint32_t vf, RowState &st, bool masked,
+                                             const int (&pos)[4], int first, int reach, int sinks) {
+    uint32_t raw[2][16];
+    ScoreBlock b;
+    int q = 0;
+    if (!masked) {
+        tmem_ld_frag(ts, raw[0]);
+#pragma unroll 1
+        for (; q < 4; ++q) {
+            block_scores(ts, kf, q, st, raw, b);
+            if (block_raises(st, b)) break;
+            block_weights(ts, vf, q, st, b);
+        }
+        tmem_wait16(raw[0]);
+        if (q == 4) return;
+    }
+    tmem_ld_frag(ts + 32u * q, raw[0]);
+#pragma unroll 1
+    for (; q < 4; ++q) {
+        block_scores(ts, kf, q, st, raw, b);
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float t = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = first + 32 * q + 8 * j, d = pos[i] - c;
+                    float2 y = of_pair(b.x[i >> 1][2 * j + (i & 1)]);
+                    if (!(d >= 0 && (d < reach || c < sinks))) y.x = -INFINITY;
+                    if (!(d >= 1 && (d - 1 < reach || c + 1 < sinks))) y.y = -INFINITY;
+                    b.x[i >> 1][2 * j + (i & 1)] = pair_of(y.x, y.y);
+                    t = fmaxf(t, fmaxf(y.x, y.y));
+                }
+                b.top[i >> 1][i & 1] = t;
+            }
+        }
+        if (block_raises(st, b)) {
+            float al[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float t = b.top[i >> 1][i & 1];
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));   // of the row
+                float up = 0.0f;
+                al[i] = 1.0f;
+                if (st.fresh >> i & 1u) {
+                    if (t > -INFINITY) up = t, st.fresh &= ~(1u << i);
+                } else if (t > kChSlack) {
+                    up = ceilf(t);
+                    al[i] = up < 126.0f ? __int_as_float((127 - (int)up) << 23) : 0.0f;
+                    st.l[i] = mul2(st.l[i], pair_of(al[i], al[i]));
+                    st.f[i] *= al[i];
+                }
+                st.m[i] += up;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    b.x[i >> 1][2 * j + (i & 1)] = add2(b.x[i >> 1][2 * j + (i & 1)], pair_of(-up, -up));
+            }
+            // The step's weights stored so far.
+#pragma unroll 1
+            for (int o = 0; o < q; ++o)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const __half2 a0 = __float2half2_rn(al[2 * hh]), a1 = __float2half2_rn(al[2 * hh + 1]);
+                    uint32_t pk[8];
+                    tmem_ld_half_frag_wait(ts + ((uint32_t)hh << 20) + 16u * o, pk);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        pk[j] = half2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&pk[j]), j & 1 ? a1 : a0));
+                    tmem_st_half_frag(ts + ((uint32_t)hh << 20) + 16u * o, pk);
+                }
+        }
+        block_weights(ts, vf, q, st, b);
+    }
+    tmem_wait16(raw[0]);
 }
 
 template <int D>
@@ -299,15 +588,14 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     constexpr int CPT = DB / 16;                 // 16-byte code chunks per token
     constexpr int CPL = kChKeys * CPT / 128;     // chunks per unpacking thread and tile
     constexpr uint32_t kColS = 0, kColO = 256;   // TMEM: S0, S1 (P in their first halves), O0, O1
-    constexpr float kNone = -1e30f;
     const PagedAttnParams &p = w.a;
     extern __shared__ uint8_t ch_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ch_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ ChunkBars bars;
     __shared__ uint32_t tmem_s;
     __shared__ volatile int abort_s;
     __shared__ float es_s[4], unit_s[4];   // per step (mod 4): 2^(E_old - E_new), 2^(E_new - 8)
     __shared__ uint32_t emax_s[2][4];
+    __shared__ float2 stats_s[8][32];      // rows' maxima and sums at a piece's end
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
     const Watchdog wd{&abort_s, p.status};
@@ -326,7 +614,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         mbar_init(&bars.drain, 1);
         mbar_fence_init();
     }
-    if (warp == 12) {
+    if (warp == 16) {
         tmem_alloc(&tmem_s, 512);
         tmem_relinquish();
     }
@@ -334,8 +622,8 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_s;
-    const uint32_t base = smem_u32(smem);
-    float *factors = reinterpret_cast<float *>(smem + L::kF);
+    const uint32_t base = (smem_u32(ch_raw) + 1023u) & ~1023u;
+    const uint32_t factors = base + (uint32_t)L::kF;
 
     const int pieces = w.division[p.B];
     // What this CTA's earlier pieces used of each barrier: steps, steps with a
@@ -390,7 +678,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
 
     if (wg < 2) {
         // ---------------------------------------------------------- softmax
-        regs_inc<192>();
+        regs_inc<kRegsSoftmax>();
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's TMEM lanes
         const uint32_t ts = tmem + kColS + 128u * wg + lanes, to = tmem + kColO + (uint32_t)(D * wg) + lanes;
         const int row = tid & 127;
@@ -420,77 +708,46 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 mbar_arrive(&bars.q);
             }
             if (!active) return;
-            const int pos = r.kv - r.n + token;
             const int pos_lo = r.kv - r.n + (tile * kChRows + wg * 128) / p.G;
             const int pos_hi = r.kv - r.n + (tile * kChRows + min(wg * 128 + 128, rows) - 1) / p.G;
-            float m = kNone, l = 0.0f, unit = 0.0f;
+            // The thread's rows in the products' layout: 8 i + lane / 4 of the warp's.
+            int pos[4];
+            RowState rs;
+            rs.fresh = 15u;
+            float unit = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rs.m[i] = 0.0f, rs.l[i] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pos[i] = r.kv - r.n + (tile * kChRows + wg * 128 + 32 * (warp & 3) + 8 * i + (lane >> 2)) / p.G;
             for (int k = k0; k < k1; ++k) {
                 const uint32_t s = step_at + (uint32_t)(k - k0);
                 const uint32_t si = wg ? step1_at + (uint32_t)(k - k0) : s;
                 const int t0 = key_of(c.st, k);
                 if (!warp_wait(&bars.s_full[wg], si & 1, wd, kSiteChunkS, (int)s)) return;
                 tc_fence_after();
-                const float *kf = factors + (s & 3) * 2 * kChKeys, *vf = kf + kChKeys;
-                float x[kChKeys];
-                float mx = m;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t raw[32];
-                    tmem_ld32_wait(ts + 32u * q, raw);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(kf + 32 * q + i);
-                        x[32 * q + i] = __uint_as_float(raw[i]) * f.x;
-                        x[32 * q + i + 1] = __uint_as_float(raw[i + 1]) * f.y;
-                        x[32 * q + i + 2] = __uint_as_float(raw[i + 2]) * f.z;
-                        x[32 * q + i + 3] = __uint_as_float(raw[i + 3]) * f.w;
-                    }
-                }
+                const uint32_t kf = factors + 4 * ((s & 3) * 2 * kChKeys + 2 * (lane & 3)), vf = kf + 4 * kChKeys;
                 const bool whole = t0 + kChKeys - 1 <= pos_lo &&
                                    (p.window == 0 || pos_hi - t0 < p.window || t0 + kChKeys <= p.sinks);
-                if (!whole) {
-#pragma unroll
-                    for (int i = 0; i < kChKeys; ++i) {
-                        const int d = pos - t0 - i;
-                        if (!(d >= 0 && (p.window == 0 || d < p.window || t0 + i < p.sinks))) x[i] = -INFINITY;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kChKeys; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
-                // A maximum that grew by much, or larger value scales:
-                // the output accumulated so far changes its unit.
                 const float es = es_s[s & 3];
                 unit = unit_s[s & 3];
-                const bool raise = mx > m + kChSlack;
-                if (__any_sync(0xffffffffu, raise) || es != 1.0f) {
-                    const float mn = raise ? mx : m, al = ex2_approx(m - mn);
-                    m = mn;
-                    l *= al;
-                    if (k > k0) {
-                        const float f = al * es;
 #pragma unroll
-                        for (int q = 0; q < D; q += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_wait(to + q, o);
+                for (int i = 0; i < 4; ++i) rs.f[i] = es;
+                softmax_rows(ts, kf, vf, rs, !whole, pos, t0 + 2 * (lane & 3), p.window ? p.window : INT32_MAX, p.sinks);
+                const bool change = rs.f[0] != 1.0f || rs.f[1] != 1.0f || rs.f[2] != 1.0f || rs.f[3] != 1.0f;
+                if (k > k0 && __any_sync(0xffffffffu, change)) {
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 32)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st32_wait(to + q, o);
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t o[16];
+                            tmem_ld_frag(to + ((uint32_t)hh << 20) + q, o);
+                            tmem_wait16(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * rs.f[2 * hh + (i >> 1 & 1)]);
+                            tmem_st_frag(to + ((uint32_t)hh << 20) + q, o);
                         }
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(vf + 32 * q + i);
-                        const float a0 = ex2_approx(x[32 * q + i] - m), a1 = ex2_approx(x[32 * q + i + 1] - m);
-                        const float a2 = ex2_approx(x[32 * q + i + 2] - m), a3 = ex2_approx(x[32 * q + i + 3] - m);
-                        l += (a0 + a1) + (a2 + a3);
-                        pk[i / 2] = half2_bits(__floats2half2_rn(a0 * f.x, a1 * f.y));
-                        pk[i / 2 + 1] = half2_bits(__floats2half2_rn(a2 * f.z, a3 * f.w));
-                    }
-                    tmem_st16(ts + 16u * q, pk);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -500,7 +757,19 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 if (!warp_wait(&bars.o_full[wg], (wg ? out1_at : out_at) & 1, wd, kSiteChunkO, (int)piece_at)) return;
                 tc_fence_after();
             }
-            const float f = slot >= 0 ? unit : l > 0.0f ? unit / l : 0.0f;
+            // Each row's maximum and sum, for the thread that writes the row.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = of_pair(rs.l[i]);
+                float x = v.x + v.y;
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if ((lane & 3) == 0) stats_s[warp][8 * i + (lane >> 2)] = make_float2(rs.m[i], x);
+            }
+            __syncwarp();
+            const float row_max = stats_s[warp][lane].x, row_sum = stats_s[warp][lane].y;
+            __syncwarp();
+            const float f = slot >= 0 ? unit : row_sum > 0.0f ? unit / row_sum : 0.0f;
             __half *out = p.out + (int64_t)(r.row0 + token) * p.out_stride + (int64_t)head * D;
             float *part_o = w.part + ((int64_t)slot * w.slot_rows + wg * 128 + row) * D;
 #pragma unroll
@@ -530,224 +799,235 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             if (slot >= 0) {
                 if (in) {
                     float2 *ml = reinterpret_cast<float2 *>(w.part + (int64_t)kChSlots * w.slot_rows * D);
-                    ml[(int64_t)slot * w.slot_rows + wg * 128 + row] = make_float2(m, l);
+                    ml[(int64_t)slot * w.slot_rows + wg * 128 + row] = make_float2(row_sum > 0.0f ? row_max : -INFINITY, row_sum);
                 }
                 if (wg == 0 && row == 0)
                     *reinterpret_cast<int4 *>(w.slots + 4 * slot) = make_int4(c.b, h, tile, c.part == 0 ? c.parts : 0);
             }
             tc_fence_before();   // the next piece's products come after these reads
         });
-    } else if (wg == 2) {
+    } else if (wg < 4) {
         // ---------------------------------------------------------- unpack
-        regs_dec<88>();
+        // One warpgroup each for K and V, alike: codes to FP16, the
+        // scales to factors of the scores or of the weights.
+        regs_dec<kRegsUnpack>();
+        const bool value = wg == 3;
         const int t = tid & 127;
-        const int tk = t / CPT, j = t % CPT;       // chunk j of tokens tk + (128 / CPT) i
+        // A thread unpacks chunk j (16 bytes, 32 dims) of the tokens
+        // tk + 128 / CPT i: two lanes read a 32-byte half of a token's codes,
+        // and the stores of 8 lanes touch every bank once.
+        const int j = D == 128 ? 2 * (warp & 1) + (lane & 1) : lane & 1;
+        const int tk = D == 128 ? 16 * ((warp >> 1) & 1) + (lane >> 1) : t >> 1;
+        constexpr int kStride = 128 / CPT;
         const int page_mask = (1 << p.page_shift) - 1;
-        const uint32_t page_vecs = (uint32_t)p.Hkv << p.page_shift;
-        float *zf = reinterpret_cast<float *>(smem + L::kZ);
-        uint32_t *zeros = reinterpret_cast<uint32_t *>(zf);
+        const uint32_t page_vecs = (uint32_t)p.Hkv << p.page_shift, page_bytes = page_vecs * DB;
+        const uint32_t last_page = (uint32_t)p.n_pages - 1u;
+        const uint8_t *codes = value ? p.v_codes : p.k_codes;
+        const uint32_t *params = reinterpret_cast<const uint32_t *>(value ? p.v_params : p.k_params);
+        const uint32_t zeros = base + (uint32_t)(L::kZ + (value ? 4 * 2 * kChKeys : 0));
+        uint64_t *full = value ? bars.v_full : bars.k_full, *empty = value ? bars.v_free : bars.k_free;
+        // Where the thread's four groups of 8 dims of its first token go.
+        uint32_t to[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            to[x] = base + (uint32_t)((value ? L::kV : L::kK) + tk * 128 + (j >> 1) * L::kPanel +
+                                      (((4 * (j & 1) + x) ^ (tk & 7)) << 4));
+        // Steps start at multiples of 128 tokens, so a token's place within
+        // its page and its table entry relative to the step's first do not
+        // change from step to step (pages of 256 tokens: but for 128).
+        int part[CPL];   // table entries past the step's first: of the chunks
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) part[i] = (tk + i * kStride) >> p.page_shift;
+        const int part_t = t >> p.page_shift;   // of token t
         walk([&](const ChunkPiece &pc) {
             const PagedRequest &r = pc.r;
-            const int b = pc.b, h = pc.h, k0 = pc.k0, k1 = pc.k1;
+            const int b = pc.b, k0 = pc.k0, k1 = pc.k1;
             const int32_t *table = p.block_table + (int64_t)b * p.max_pages;
-            const uint8_t *kc = p.k_codes + ((int64_t)h << p.page_shift) * DB + j * 16;
-            const uint8_t *vc = p.v_codes + ((int64_t)h << p.page_shift) * DB + j * 16;
-            auto page_of = [&](int key) {   // -1 past the end and outside the cache
-                int page = -1;
-                if (key < r.kv) {
-                    page = __ldg(table + (key >> p.page_shift));
-                    if ((uint32_t)page >= (uint32_t)p.n_pages) {
+            const int last_entry = (r.kv - 1) >> p.page_shift;   // there is a step only where r.kv > 0
+            const uint32_t head_vec = (uint32_t)pc.h << p.page_shift;
+            const uint8_t *from[CPL];   // the chunks' places in page 0
+#pragma unroll
+            for (int i = 0; i < CPL; ++i)
+                from[i] = codes + ((uint64_t)head_vec + ((tk + i * kStride) & page_mask)) * DB + j * 16;
+            const uint32_t *from_t = params + head_vec + (t & page_mask);
+            // Table entries are loaded a step before anything depends on them.
+            struct Pages {
+                int chunk[CPL], token;
+            };
+            auto load_pages = [&](int k, Pages &g) {
+                const int first = key_of(pc.st, min(k, k1 - 1)) >> p.page_shift;
+#pragma unroll
+                for (int i = 0; i < CPL; ++i) g.chunk[i] = __ldg(table + min(first + part[i], last_entry));
+                g.token = __ldg(table + min(first + part_t, last_entry));
+            };
+            // Step k's codes of this thread. Numbers outside the cache read
+            // its last page, which scales of 0 make nothing of.
+            auto load_codes = [&](int k, const Pages &g, uint4 (&u)[CPL]) {
+                const uint32_t more = p.page_shift == 8 ? (uint32_t)(key_of(pc.st, min(k, k1 - 1)) & 128) * DB : 0u;
+#pragma unroll
+                for (int i = 0; i < CPL; ++i)
+                    u[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        from[i] + (uint64_t)min((uint32_t)g.chunk[i], last_page) * page_bytes + more));
+            };
+            auto load_sz = [&](int k, int page) {   // token t's scale and zero
+                uint32_t sz = 0u;
+                const int key = key_of(pc.st, k) + t;
+                if (k < k1 && key < r.kv) {
+                    if ((uint32_t)page <= last_page)
+                        sz = __ldg(from_t + (uint64_t)(uint32_t)page * page_vecs + (p.page_shift == 8 ? (key - t) & 128 : 0));
+                    else
                         paged_bad_request(p, b);
-                        page = -1;
-                    }
                 }
-                return page;
+                return sz;
             };
-            // One tile's codes of one tensor, each thread its own chunks to
-            // its own places; parts without a page copy page 0's.
-            uint32_t put = 0, get = 0;   // ring places
-            auto fetch = [&](int half) {   // half steps: keys of step k0 + half / 2, then its values
-                const int k = k0 + (half >> 1);
-                if (k < k1) {
-                    const int t0 = key_of(pc.st, k) + tk;
-                    const uint8_t *c = half & 1 ? vc : kc;
-                    const uint32_t dst = base + (uint32_t)(L::kC + t * 16) + put;
-#pragma unroll
-                    for (int i = 0; i < CPL; ++i) {
-                        const int key = t0 + i * (128 / CPT);
-                        const int page = max(page_of(key), 0);
-                        copy16(dst + (uint32_t)(i * 2048), c + (uint64_t)(uint32_t)page * (page_vecs * DB) + (key & page_mask) * DB);
-                    }
-                }
-                copy_commit();
-                put = put + L::kCodes == L::kRing * L::kCodes ? 0 : put + L::kCodes;
-            };
-            auto load_sz = [&](int k, uint32_t &kw, uint32_t &vw) {   // token t's scale and zero
-                kw = vw = 0u;
-                if (k < k1) {
-                    const int key = key_of(pc.st, k) + t;
-                    const int page = page_of(key);
-                    if (page >= 0) {
-                        const uint64_t at = (uint64_t)(uint32_t)page * page_vecs + ((uint32_t)h << p.page_shift) + (key & page_mask);
-                        kw = __ldg(reinterpret_cast<const uint32_t *>(p.k_params) + at);
-                        vw = __ldg(reinterpret_cast<const uint32_t *>(p.v_params) + at);
-                    }
-                }
-            };
-            // Codes of the ring's next tile -> FP16 c - z in the stage at dst.
-            auto unpack = [&](uint32_t dst, const uint32_t *z) {
-                const uint32_t src = base + (uint32_t)(L::kC + t * 16) + get;
-                get = get + L::kCodes == L::kRing * L::kCodes ? 0 : get + L::kCodes;
-#pragma unroll
-                for (int i = 0; i < CPL; ++i) {
-                    const int token = tk + i * (128 / CPT);
-                    const uint4 u = lds128(src + (uint32_t)(i * 2048));
-                    const uint32_t zz = z[token];   // halves 1024 + z, 64 + z
-                    const uint32_t z1 = __byte_perm(zz, zz, 0x1010), z2 = __byte_perm(zz, zz, 0x3232);
-                    const uint32_t words[4] = {u.x, u.y, u.z, u.w};
-                    const uint32_t row = dst + (uint32_t)(token * 128 + (j >> 1) * L::kPanel);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        // In an order in which 8 threads' stores touch every bank once.
-                        const int e = x ^ (j & 2);
-                        const uint32_t c = j & 2 ? words[x ^ 2] : words[x], c8 = c >> 8;
-                        sts128(row + (uint32_t)(((4 * (j & 1) + e) ^ (token & 7)) << 4),
-                               hsub2((c & 0x000F000Fu) | 0x64006400u, z1), hsub2((c & 0x00F000F0u) | 0x54005400u, z2),
-                               hsub2((c8 & 0x000F000Fu) | 0x64006400u, z1), hsub2((c8 & 0x00F000F0u) | 0x54005400u, z2));
-                    }
-                }
-            };
-            uint32_t kw, vw;
-            load_sz(k0, kw, vw);
-            fetch(0);
-            fetch(1);
-            fetch(2);
+            if (k0 == k1) return;
+            uint4 u[CPL], un[CPL];   // codes of this step and the next
+            Pages g;                 // entries of the next step
+            load_pages(k0, g);
+            load_codes(k0, g, u);
+            uint32_t sz = load_sz(k0, g.token);
+            load_pages(k0 + 1, g);
             int eb = 103;   // 127 + the exponent of the largest value scale so far (scales >= 2^-24)
+            bool ok = true;
+#pragma unroll 1
             for (int k = k0; k < k1; ++k) {
                 const uint32_t s = step_at + (uint32_t)(k - k0), stage = s & 1;
+                const uint32_t z = zeros + 4 * stage * kChKeys;
                 // The step's factors. A written scale is finite and a zero at
                 // most 15; the bounds make a hidden token's values
                 // so too, whatever it holds, so that its weight 0 stays 0.
-                const uint32_t sv = min(vw & 0xFFFFu, 0x7BFFu);
-                const float zk = fminf(fmaxf(__half2float(half_hi(kw)), 0.0f), 15.0f);
-                const float zv = fminf(fmaxf(__half2float(half_hi(vw)), 0.0f), 15.0f);
-                const uint32_t wmax = __reduce_max_sync(0xffffffffu, sv);
-                if (lane == 0) emax_s[stage][warp & 3] = wmax;
-                zeros[t] = half2_bits(__floats2half2_rn(1024.0f + zk, 64.0f + zk));
-                zeros[kChKeys + t] = half2_bits(__floats2half2_rn(1024.0f + zv, 64.0f + zv));
-                named_bar_sync(1, 128);
-                const uint32_t top = max(max(emax_s[stage][0], emax_s[stage][1]), max(emax_s[stage][2], emax_s[stage][3]));
-                const int ebn = max(eb, (int)(__float_as_uint(half_lo(top)) >> 23));
-                float *kf = factors + (s & 3) * 2 * kChKeys;
-                kf[t] = half_lo(kw) * p.qscale;
-                kf[kChKeys + t] = half_lo(sv) * __int_as_float((262 - ebn) << 23);   // 2^(8 - E)
-                if (t == 0) {
-                    es_s[s & 3] = __int_as_float((127 + eb - ebn) << 23);
-                    unit_s[s & 3] = __int_as_float((ebn - 8) << 23);
+                const uint32_t scale = value ? min(sz & 0xFFFFu, 0x7BFFu) : sz & 0xFFFFu;
+                const float zero = fminf(fmaxf(__half2float(half_hi(sz)), 0.0f), 15.0f);
+                sts32(z + 4 * t, half2_bits(__floats2half2_rn(1024.0f + zero, 64.0f + zero)));
+                if (value) {
+                    const uint32_t wmax = __reduce_max_sync(0xffffffffu, scale);
+                    if (lane == 0) emax_s[stage][warp & 3] = wmax;
                 }
-                eb = ebn;
-                load_sz(k + 1, kw, vw);
-                const uint32_t freed = ((s >> 1) - 1) & 1;
-                // Keys.
-                bool ok = s < 2 || wait_bounded(&bars.k_free[stage], freed, wd, kSiteChunkFree, (int)s);
-                copy_wait<2>();
+                // The only meeting of a step: zeros and maxima are double-buffered.
+                if (named_bar_any(2 + (value ? 1 : 0), 128, !ok)) break;
+                const uint32_t f = factors + 4 * ((s & 3) * 2 * kChKeys + t);
+                if (value) {
+                    const uint32_t top = max(max(emax_s[stage][0], emax_s[stage][1]), max(emax_s[stage][2], emax_s[stage][3]));
+                    const int ebn = max(eb, (int)(__float_as_uint(half_lo(top)) >> 23));
+                    sts32f(f + 4 * kChKeys, half_lo(scale) * __int_as_float((262 - ebn) << 23));   // 2^(8 - E)
+                    if (t == 0) {
+                        es_s[s & 3] = __int_as_float((127 + eb - ebn) << 23);
+                        unit_s[s & 3] = __int_as_float((ebn - 8) << 23);
+                    }
+                    eb = ebn;
+                } else {
+                    sts32f(f, half_lo(scale) * p.qscale);
+                }
+                sz = load_sz(k + 1, g.token);
+                load_codes(k + 1, g, un);
+                load_pages(k + 2, g);
+                uint32_t zz[CPL];
+#pragma unroll
+                for (int i = 0; i < CPL; ++i) zz[i] = lds32(z + 4 * (tk + i * kStride));   // halves 1024 + z, 64 + z
+                ok = s < 2 || wait_long(&empty[stage], ((s >> 1) - 1) & 1, wd, kSiteChunkFree, (int)s);
                 if (ok) {
-                    unpack(base + L::kK + stage * L::kTile, zeros);
+                    uint32_t dst[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) dst[x] = to[x] + stage * (uint32_t)L::kTile;
+                    auto unpack = [&](auto index) {
+                        constexpr int i = decltype(index)::value;
+                        const uint32_t z1 = __byte_perm(zz[i], zz[i], 0x1010), z2 = __byte_perm(zz[i], zz[i], 0x3232);
+                        const uint32_t words[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t c = words[x], c8 = c >> 8;
+                            sts128_at<i * kStride * 128>(
+                                dst[x], hsub2((c & 0x000F000Fu) | 0x64006400u, z1), hsub2((c & 0x00F000F0u) | 0x54005400u, z2),
+                                hsub2((c8 & 0x000F000Fu) | 0x64006400u, z1), hsub2((c8 & 0x00F000F0u) | 0x54005400u, z2));
+                        }
+                    };
+                    unpack(Index<0>());
+                    unpack(Index<1>());
+                    if constexpr (CPL == 4) {
+                        unpack(Index<2>());
+                        unpack(Index<3>());
+                    }
                     fence_proxy_async_smem();
-                    mbar_arrive(&bars.k_full[stage]);
+                    mbar_arrive(&full[stage]);
                 }
-                fetch(2 * (k - k0) + 3);
-                // Values.
-                ok = ok && (s < 2 || wait_bounded(&bars.v_free[stage], freed, wd, kSiteChunkFree, (int)s));
-                copy_wait<2>();
-                if (ok) {
-                    unpack(base + L::kV + stage * L::kTile, zeros + kChKeys);
-                    fence_proxy_async_smem();
-                    mbar_arrive(&bars.v_full[stage]);
-                }
-                fetch(2 * (k - k0) + 4);
-                if (named_bar_any(1, 128, !ok)) break;   // and the zeros are read
+#pragma unroll
+                for (int i = 0; i < CPL; ++i) u[i] = un[i];
             }
-            copy_wait<0>();
         });
     } else {
         // ---------------------------------------------------------- issue
-        regs_dec<40>();
+        regs_dec<kRegsIssue>();
         walk([&](const ChunkPiece &c) {
-            if (warp != 12) return;
+            if (warp != 16) return;
             const int steps = c.k1 - c.k0;
             const bool two = c.rows > 128;
             constexpr uint32_t id_s = idesc_f16(128, kChKeys, false), id_o = idesc_f16(128, D, true);
-            bool ok = warp_wait(&bars.q, piece_at & 1, wd, kSiteChunkQ, (int)piece_at);
-            auto scores = [&](int i, uint32_t stage) {
-                if (lane == 0) {
+            if (lane == 0) {
+                bool ok = wait_bounded(&bars.q, piece_at & 1, wd, kSiteChunkQ, (int)piece_at);
+                const uint64_t qd = smem_desc_k_sw128(base + L::kQ), kd = smem_desc_k_sw128(base + L::kK);
+                const uint64_t vd = smem_desc_mn_sw128(base + L::kV, L::kPanel);
+                auto scores = [&](int i, uint32_t stage) {
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint32_t o = (uint32_t)((x >> 2) * L::kPanel + (x & 3) * 32);
-                        mma_f16_ss(tmem + kColS + 128u * i, smem_desc_k_sw128(base + L::kQ + i * L::kTile + o),
-                                   smem_desc_k_sw128(base + L::kK + stage * L::kTile + o), id_s, x > 0);
-                    }
+                    for (int x = 0; x < D / 64; ++x)
+                        mma4_f16_ss(tmem + kColS + 128u * i, qd + (uint64_t)((i * L::kTile + x * L::kPanel) >> 4),
+                                    kd + (uint64_t)((stage * L::kTile + x * L::kPanel) >> 4), id_s, x > 0);
                     tc_commit(&bars.s_full[i]);
-                }
-            };
-            auto values = [&](int i, uint32_t stage, bool first) {
-                if (lane == 0) {
+                };
+                auto values = [&](int i, uint32_t stage, bool first) {
 #pragma unroll
-                    for (int x = 0; x < kChKeys / 16; ++x)
-                        mma_f16_ts(tmem + kColO + (uint32_t)(D * i), tmem + kColS + 128u * i + 8u * x,
-                                   smem_desc_mn_sw128(base + L::kV + stage * L::kTile + x * 2048, L::kPanel), id_o,
-                                   !first || x > 0);
-                }
-            };
-            auto commit = [&](uint64_t *bar) {
-                if (lane == 0) tc_commit(bar);
-            };
-            if (ok && steps > 0) {
-                const uint32_t s0 = step_at;
-                ok = warp_wait(&bars.k_full[s0 & 1], (s0 >> 1) & 1, wd, kSiteChunkK, (int)s0);
-                if (ok) {
-                    tc_fence_after();
-                    scores(0, s0 & 1);
-                    if (two) scores(1, s0 & 1);
-                    commit(&bars.k_free[s0 & 1]);
-                }
-                for (int k = 0; ok && k < steps; ++k) {
-                    const uint32_t s = step_at + (uint32_t)k, stage = s & 1, next = stage ^ 1;
-                    const bool more = k + 1 < steps;
-                    if (!(ok = warp_wait(&bars.v_full[stage], (s >> 1) & 1, wd, kSiteChunkV, (int)s))) break;
-                    if (!(ok = warp_wait(&bars.p_full[0], s & 1, wd, kSiteChunkP, (int)s))) break;
-                    tc_fence_after();
-                    values(0, stage, k == 0);
-                    if (!more) commit(&bars.o_full[0]);
-                    if (more) {
-                        if (!(ok = warp_wait(&bars.k_full[next], ((s + 1) >> 1) & 1, wd, kSiteChunkK, (int)s + 1))) break;
+                    for (int x = 0; x < kChKeys / 64; ++x)
+                        mma4_f16_ts(tmem + kColO + (uint32_t)(D * i), tmem + kColS + 128u * i + 32u * x,
+                                    vd + (uint64_t)((stage * L::kTile + x * 64 * 128) >> 4), id_o, !first || x > 0);
+                };
+                if (ok && steps > 0) {
+                    const uint32_t s0 = step_at;
+                    ok = wait_bounded(&bars.k_full[s0 & 1], (s0 >> 1) & 1, wd, kSiteChunkK, (int)s0);
+                    if (ok) {
                         tc_fence_after();
-                        scores(0, next);
+                        scores(0, s0 & 1);
+                        if (two) scores(1, s0 & 1);
+                        tc_commit(&bars.k_free[s0 & 1]);
                     }
-                    if (two) {
-                        if (!(ok = warp_wait(&bars.p_full[1], (step1_at + (uint32_t)k) & 1, wd, kSiteChunkP, (int)s))) break;
+                    for (int k = 0; ok && k < steps; ++k) {
+                        const uint32_t s = step_at + (uint32_t)k, stage = s & 1, next = stage ^ 1;
+                        const bool more = k + 1 < steps;
+                        if (!(ok = wait_bounded(&bars.v_full[stage], (s >> 1) & 1, wd, kSiteChunkV, (int)s))) break;
+                        if (!(ok = wait_bounded(&bars.p_full[0], s & 1, wd, kSiteChunkP, (int)s))) break;
                         tc_fence_after();
-                        values(1, stage, k == 0);
-                        if (!more) commit(&bars.o_full[1]);
-                    }
-                    commit(&bars.v_free[stage]);
-                    if (more) {
-                        if (two) scores(1, next);
-                        commit(&bars.k_free[next]);
+                        values(0, stage, k == 0);
+                        if (more) {
+                            if (!(ok = wait_bounded(&bars.k_full[next], ((s + 1) >> 1) & 1, wd, kSiteChunkK, (int)s + 1))) break;
+                            tc_fence_after();
+                            scores(0, next);
+                        } else {
+                            tc_commit(&bars.o_full[0]);
+                        }
+                        if (two) {
+                            if (!(ok = wait_bounded(&bars.p_full[1], (step1_at + (uint32_t)k) & 1, wd, kSiteChunkP, (int)s)))
+                                break;
+                            tc_fence_after();
+                            values(1, stage, k == 0);
+                            if (!more) tc_commit(&bars.o_full[1]);
+                        }
+                        tc_commit(&bars.v_free[stage]);
+                        if (more) {
+                            if (two) scores(1, next);
+                            tc_commit(&bars.k_free[next]);
+                        }
                     }
                 }
-            }
-            if (!ok && lane == 0) {
-                // Let the products in flight end before the memory is given back.
-                tc_commit(&bars.drain);
-                wait_drain(&bars.drain, 0, kWaitLimitNs);
+                if (!ok) {
+                    // Let the products in flight end before the memory is given back.
+                    tc_commit(&bars.drain);
+                    wait_drain(&bars.drain, 0, kWaitLimitNs);
+                }
             }
             __syncwarp();
         });
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -778,7 +1058,7 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_consta
         for (int i = 0; i < parts; ++i) {
             const int64_t at = (int64_t)(slot + i) * w.slot_rows + row;
             const float2 x = ml[at];
-            const float f = exp2f(x.x - m);
+            const float f = x.y > 0.0f ? exp2f(x.x - m) : 0.0f;
             l += f * x.y;
             const float *src = w.part + at * D + lane * (D / 32);
 #pragma unroll
