@@ -199,33 +199,50 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn) {
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Shared-memory operand descriptors with the 128-byte swizzle, as their low
+// words (start address, and the stride between 64-element panels for operands
+// whose M or N index is contiguous); the high word is the same for all: 1024
+// bytes between groups of 8 rows, version 1, swizzle 2.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t panel) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((panel >> 4) << 16);
+}
+
 // D (+)= A . B over 64 of the inner index, both operands in shared memory with
 // that index contiguous: four products of 16, 32 bytes apart in a swizzled row.
-__device__ __forceinline__ void mma4_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The descriptors are put together inside, so that they are not all kept in
+// registers across the loop.
+__device__ __forceinline__ void mma4_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 u, v;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %3, 1;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %3, 1;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %9, %10, %3, 1;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "l"(a + 2ull), "l"(b + 2ull), "l"(a + 4ull), "l"(b + 4ull),
-        "l"(a + 6ull), "l"(b + 6ull)
+        "mov.b64 u, {%1, %5};\n\tmov.b64 v, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, 1;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, 1;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 u, {x, %5};\n\tmov.b64 v, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, 1;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
         : "memory");
 }
 
 // D (+)= A . B over 64 keys: A in tensor memory (8 columns per 16 keys), B
 // with its N index contiguous (2048 bytes per 16 keys).
-__device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 v;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %3, 1;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %3, 1;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %3, 1;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(a + 8u), "l"(b + 128ull), "r"(a + 16u), "l"(b + 256ull),
-        "r"(a + 24u), "l"(b + 384ull)
+        "mov.b64 v, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], v, %3, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 v, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, 1;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 v, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, 1;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 v, {y, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, 1;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
         : "memory");
 }
 
@@ -257,19 +274,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-
-// Shared-memory descriptor of an operand whose M or N index is contiguous:
-// 128-byte swizzle, blocks of 64 (contiguous) x 8 elements; `panel` bytes to the
-// next 64 along the contiguous index, 1024 to the next 8 along the other.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t panel) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(panel >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
 }
 
 // Loads of 16 lanes x 32 columns in the layout of matrix fragments: lane t's
@@ -371,7 +375,7 @@ struct ChunkSmem {
 };
 
 struct ChunkBars {
-    uint64_t q, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], drain;
 };
 
 enum ChunkSite : int {
@@ -500,12 +504,13 @@ __device__ __forceinline__ bool block_raises(const RowState &st, const ScoreBloc
 //
 // A row's maximum is raised only when a score exceeds it by 2^kChSlack, by a
 // whole number, so that what is already stored is rescaled exactly; a row takes
-// its first maximum as it is. Key k, counted from the lane's first one, which
-// stands at position `first`, is hidden from row i where first + k > pos[i], or
-// beyond the window (pos[i] - first - k >= reach) and the sinks
-// (first + k >= sinks).
+// its first maximum as it is. The step's keys stand at positions key0 .. key0 +
+// 127; the key at c is hidden from row i where c > pos[i], or beyond the window
+// (pos[i] - c >= reach) and the sinks (c >= sinks). pos_lo and pos_hi: the least
+// and largest of the warp's rows.
 __device__ __forceinline__ void softmax_rows(uint32_t ts, uint32_t kf, uint32_t vf, RowState &st, bool masked,
-                                             const int (&pos)[4], int first, int reach, int sinks) {
+                                             const int (&pos)[4], int pos_lo, int pos_hi, int key0, int reach,
+                                             int sinks) {
     uint32_t raw[2][16];
     ScoreBlock b;
     int q = 0;
@@ -523,17 +528,29 @@ __device__ __forceinline__ void softmax_rows(uint32_t ts, uint32_t kf, uint32_t 
     tmem_ld_frag(ts + 32u * q, raw[0]);
 #pragma unroll 1
     for (; q < 4; ++q) {
+        // What of the block the warp's rows see: all of it, none, or some.
+        const int c0 = key0 + 32 * q;
+        const bool whole = c0 + 31 <= pos_lo && (pos_hi - c0 < reach || c0 + 32 <= sinks);
+        if (c0 > pos_hi || (pos_lo - c0 - 31 >= reach && c0 >= sinks)) {
+            const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            tmem_wait16(raw[0]);
+            tmem_st_half_frag(ts + 16u * q, none);
+            tmem_st_half_frag(ts + (1u << 20) + 16u * q, none);
+            tmem_ld_frag(ts + 32u * ((q + 1) & 3), raw[0]);
+            continue;
+        }
         block_scores(ts, kf, q, st, raw, b);
-        if (masked) {
+        if (!whole) {
+            const int first = c0 + 2 * ((int)threadIdx.x & 3);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float t = -INFINITY;
+                const int d = pos[i] - first;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = first + 32 * q + 8 * j, d = pos[i] - c;
                     float2 y = of_pair(b.x[i >> 1][2 * j + (i & 1)]);
-                    if (!(d >= 0 && (d < reach || c < sinks))) y.x = -INFINITY;
-                    if (!(d >= 1 && (d - 1 < reach || c + 1 < sinks))) y.y = -INFINITY;
+                    if (!(d >= 8 * j && (d - 8 * j < reach || first + 8 * j < sinks))) y.x = -INFINITY;
+                    if (!(d >= 8 * j + 1 && (d - 8 * j - 1 < reach || first + 8 * j + 1 < sinks))) y.y = -INFINITY;
                     b.x[i >> 1][2 * j + (i & 1)] = pair_of(y.x, y.y);
                     t = fmaxf(t, fmaxf(y.x, y.y));
                 }
@@ -595,14 +612,15 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     __shared__ volatile int abort_s;
     __shared__ float es_s[4], unit_s[4];   // per step (mod 4): 2^(E_old - E_new), 2^(E_new - 8)
     __shared__ uint32_t emax_s[2][4];
+    __shared__ ChunkPiece piece_s[kChThreads / 32][2];   // each warp's piece, and the softmaxes' next
     __shared__ float2 stats_s[8][32];      // rows' maxima and sums at a piece's end
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
     const Watchdog wd{&abort_s, p.status};
     if (tid == 0) {
         abort_s = 0;
-        mbar_init(&bars.q, 256);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.q[i], 128);
             mbar_init(&bars.k_full[i], 128);
             mbar_init(&bars.k_free[i], 1);
             mbar_init(&bars.v_full[i], 128);
@@ -626,11 +644,19 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     const uint32_t factors = base + (uint32_t)L::kF;
 
     const int pieces = w.division[p.B];
-    // What this CTA's earlier pieces used of each barrier: steps, steps with a
-    // second row tile, pieces, pieces with steps, those with a second row tile.
+    // What this CTA's earlier pieces used of each barrier: steps, pieces and
+    // pieces with steps, and of each those with a second row tile.
     uint32_t step_at = 0, step1_at = 0, piece_at = 0, out_at = 0, out1_at = 0;
 
-    auto run_piece = [&](int piece, auto role) {
+    // The CTA's piece of a round, into *out (its warp's own place in shared
+    // memory, where the roles read what they need of it); false after the
+    // last. Pieces go round the CTAs forth and back: the lengths fall along the
+    // list. Every role takes them by itself, in step with the others through the
+    // barriers alone, so that the next piece's first keys are unpacked and its
+    // queries loaded while the last one's output is written.
+    auto locate = [&](int round, ChunkPiece *out) {
+        const int piece = round * (int)gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        if (__any_sync(0xffffffffu, piece >= pieces || abort_s != 0)) return false;
         int lo = 0, hi = p.B - 1;   // the last request that starts at or before the piece
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -654,22 +680,25 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         c.k0 = c.part * each + min(c.part, extra);
         c.k1 = c.k0 + each + (c.part < extra ? 1 : 0);
         c.slot = c.parts > 1 ? w.division[p.B + 1 + lo] + rest : -1;
-        role(c);
+        __syncwarp();
+        if (lane == 0) *out = c;
+        __syncwarp();
+        return true;
+    };
+    auto advance = [&](const ChunkPiece &c) {
         const uint32_t steps = (uint32_t)(c.k1 - c.k0), two = c.rows > 128 ? 1 : 0;
         step_at += steps;
         step1_at += two * steps;
         ++piece_at;
         out_at += steps > 0;
         out1_at += two & (steps > 0);
+        __syncwarp();
     };
-    // Pieces in turn, forth and back over the CTAs: the lengths fall along the list.
     auto walk = [&](auto role) {
-        for (int round = 0;; ++round) {
-            const int piece = round * (int)gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
-            if (round * (int)gridDim.x >= pieces) break;
-            if (piece < pieces) run_piece(piece, role);
-            __syncthreads();   // every role is done with the piece
-            if (abort_s) break;
+        ChunkPiece *c = &piece_s[warp][0];
+        for (int round = 0; locate(round, c); ++round) {
+            role(*c);
+            advance(*c);
         }
     };
     auto key_of = [&](const ChunkSteps &st, int k) {
@@ -682,34 +711,41 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's TMEM lanes
         const uint32_t ts = tmem + kColS + 128u * wg + lanes, to = tmem + kColO + (uint32_t)(D * wg) + lanes;
         const int row = tid & 127;
-        walk([&](const ChunkPiece &c) {
-            const PagedRequest &r = c.r;
-            const int h = c.h, tile = c.tile, rows = c.rows, k0 = c.k0, k1 = c.k1, slot = c.slot;
-            const bool active = wg * 128 < rows;
-            const int pair = tile * kChRows + wg * 128 + row;            // (token, head) pair of the request
-            const bool in = wg * 128 + row < rows;
-            const int token = pair / p.G, head = h * p.G + (pair - token * p.G);
-            // The queries, dims in unpacking order, 128-byte swizzle.
-            {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(r.row0 + token) * p.q_stride +
-                                                                   (int64_t)head * D);
-                const uint32_t dst = base + L::kQ + (uint32_t)(wg * L::kTile + row * 128);
-                if (active) {
+        // A piece's queries, a row per thread: dims in unpacking order, 128-byte swizzle.
+        auto load_q = [&](const ChunkPiece &c) {
+            if (wg * 128 >= c.rows || c.k0 == c.k1) return;
+            const int pair = c.tile * kChRows + wg * 128 + row, token = pair / p.G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(c.r.row0 + token) * p.q_stride +
+                                                               (int64_t)(c.h * p.G + pair - token * p.G) * D);
+            const uint32_t dst = base + L::kQ + (uint32_t)(wg * L::kTile + row * 128);
+            const bool in = wg * 128 + row < c.rows;
 #pragma unroll
-                    for (int x = 0; x < D / 8; ++x) {
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                        if (in) u = __ldg(src + x);
-                        sts128(dst + (uint32_t)((x >> 3) * L::kPanel + (((x & 7) ^ (row & 7)) << 4)),
-                               __byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632),
-                               __byte_perm(u.y, u.w, 0x5410), __byte_perm(u.y, u.w, 0x7632));
-                    }
+            for (int x0 = 0; x0 < D / 8; x0 += 8) {
+                uint4 u[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    u[x] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in) u[x] = __ldg(src + x0 + x);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.q);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    sts128(dst + (uint32_t)((x0 >> 3) * L::kPanel + ((x ^ (row & 7)) << 4)),
+                           __byte_perm(u[x].x, u[x].z, 0x5410), __byte_perm(u[x].x, u[x].z, 0x7632),
+                           __byte_perm(u[x].y, u[x].w, 0x5410), __byte_perm(u[x].y, u[x].w, 0x7632));
             }
-            if (!active) return;
-            const int pos_lo = r.kv - r.n + (tile * kChRows + wg * 128) / p.G;
-            const int pos_hi = r.kv - r.n + (tile * kChRows + min(wg * 128 + 128, rows) - 1) / p.G;
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.q[wg]);
+        };
+        bool have = locate(0, &piece_s[warp][0]);
+        if (have) load_q(piece_s[warp][0]);
+        for (int round = 0; have; ++round) {
+            const ChunkPiece &c = piece_s[warp][round & 1];
+            const PagedRequest &r = c.r;
+            const int tile = c.tile, k0 = c.k0, k1 = c.k1;
+            const bool active = wg * 128 < c.rows;
+            bool ok = true;
+            const int first_row = tile * kChRows + wg * 128 + 32 * (warp & 3);   // of the warp
+            const int pos_lo = r.kv - r.n + first_row / p.G, pos_hi = r.kv - r.n + (first_row + 31) / p.G;
             // The thread's rows in the products' layout: 8 i + lane / 4 of the warp's.
             int pos[4];
             RowState rs;
@@ -719,12 +755,12 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             for (int i = 0; i < 4; ++i) rs.m[i] = 0.0f, rs.l[i] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                pos[i] = r.kv - r.n + (tile * kChRows + wg * 128 + 32 * (warp & 3) + 8 * i + (lane >> 2)) / p.G;
-            for (int k = k0; k < k1; ++k) {
+                pos[i] = r.kv - r.n + (first_row + 8 * i + (lane >> 2)) / p.G;
+            for (int k = k0; active && k < k1; ++k) {
                 const uint32_t s = step_at + (uint32_t)(k - k0);
                 const uint32_t si = wg ? step1_at + (uint32_t)(k - k0) : s;
                 const int t0 = key_of(c.st, k);
-                if (!warp_wait(&bars.s_full[wg], si & 1, wd, kSiteChunkS, (int)s)) return;
+                if (!(ok = warp_wait(&bars.s_full[wg], si & 1, wd, kSiteChunkS, (int)s))) break;
                 tc_fence_after();
                 const uint32_t kf = factors + 4 * ((s & 3) * 2 * kChKeys + 2 * (lane & 3)), vf = kf + 4 * kChKeys;
                 const bool whole = t0 + kChKeys - 1 <= pos_lo &&
@@ -733,7 +769,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 unit = unit_s[s & 3];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rs.f[i] = es;
-                softmax_rows(ts, kf, vf, rs, !whole, pos, t0 + 2 * (lane & 3), p.window ? p.window : INT32_MAX, p.sinks);
+                softmax_rows(ts, kf, vf, rs, !whole, pos, pos_lo, pos_hi, t0, p.window ? p.window : INT32_MAX, p.sinks);
                 const bool change = rs.f[0] != 1.0f || rs.f[1] != 1.0f || rs.f[2] != 1.0f || rs.f[3] != 1.0f;
                 if (k > k0 && __any_sync(0xffffffffu, change)) {
 #pragma unroll 1
@@ -753,10 +789,18 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 tc_fence_before();
                 mbar_arrive(&bars.p_full[wg]);
             }
-            if (k1 > k0) {
-                if (!warp_wait(&bars.o_full[wg], (wg ? out1_at : out_at) & 1, wd, kSiteChunkO, (int)piece_at)) return;
-                tc_fence_after();
-            }
+            // The scores of the last step are in: the queries' place is free.
+            have = ok && locate(round + 1, &piece_s[warp][(round + 1) & 1]);
+            if (have) load_q(piece_s[warp][(round + 1) & 1]);
+            if (active && k1 > k0)
+                ok = ok && warp_wait(&bars.o_full[wg], (wg ? out1_at : out_at) & 1, wd, kSiteChunkO, (int)piece_at);
+            if (!ok) break;
+            advance(c);
+            if (!active) continue;
+            tc_fence_after();
+            const int pair = tile * kChRows + wg * 128 + row;   // (token, head) pair of the request
+            const bool in = wg * 128 + row < c.rows;
+            const int token = pair / p.G, head = c.h * p.G + (pair - token * p.G), slot = c.slot;
             // Each row's maximum and sum, for the thread that writes the row.
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -802,10 +846,10 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                     ml[(int64_t)slot * w.slot_rows + wg * 128 + row] = make_float2(row_sum > 0.0f ? row_max : -INFINITY, row_sum);
                 }
                 if (wg == 0 && row == 0)
-                    *reinterpret_cast<int4 *>(w.slots + 4 * slot) = make_int4(c.b, h, tile, c.part == 0 ? c.parts : 0);
+                    *reinterpret_cast<int4 *>(w.slots + 4 * slot) = make_int4(c.b, c.h, tile, c.part == 0 ? c.parts : 0);
             }
             tc_fence_before();   // the next piece's products come after these reads
-        });
+        }
     } else if (wg < 4) {
         // ---------------------------------------------------------- unpack
         // One warpgroup each for K and V, alike: codes to FP16, the
@@ -957,29 +1001,29 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     } else {
         // ---------------------------------------------------------- issue
         regs_dec<kRegsIssue>();
-        walk([&](const ChunkPiece &c) {
-            if (warp != 16) return;
+        if (warp == 16) walk([&](const ChunkPiece &c) {
             const int steps = c.k1 - c.k0;
             const bool two = c.rows > 128;
             constexpr uint32_t id_s = idesc_f16(128, kChKeys, false), id_o = idesc_f16(128, D, true);
-            if (lane == 0) {
-                bool ok = wait_bounded(&bars.q, piece_at & 1, wd, kSiteChunkQ, (int)piece_at);
-                const uint64_t qd = smem_desc_k_sw128(base + L::kQ), kd = smem_desc_k_sw128(base + L::kK);
-                const uint64_t vd = smem_desc_mn_sw128(base + L::kV, L::kPanel);
+            if (lane == 0 && steps > 0) {
+                bool ok = wait_bounded(&bars.q[0], out_at & 1, wd, kSiteChunkQ, (int)piece_at) &&
+                          (!two || wait_bounded(&bars.q[1], out1_at & 1, wd, kSiteChunkQ, (int)piece_at));
+                const uint32_t qd = desc_low(base + L::kQ, 16), kd = desc_low(base + L::kK, 16);
+                const uint32_t vd = desc_low(base + L::kV, L::kPanel);
                 auto scores = [&](int i, uint32_t stage) {
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
-                        mma4_f16_ss(tmem + kColS + 128u * i, qd + (uint64_t)((i * L::kTile + x * L::kPanel) >> 4),
-                                    kd + (uint64_t)((stage * L::kTile + x * L::kPanel) >> 4), id_s, x > 0);
+                        mma4_f16_ss(tmem + kColS + 128u * i, qd + (uint32_t)((i * L::kTile + x * L::kPanel) >> 4),
+                                    kd + (uint32_t)((stage * L::kTile + x * L::kPanel) >> 4), id_s, x > 0);
                     tc_commit(&bars.s_full[i]);
                 };
                 auto values = [&](int i, uint32_t stage, bool first) {
 #pragma unroll
                     for (int x = 0; x < kChKeys / 64; ++x)
                         mma4_f16_ts(tmem + kColO + (uint32_t)(D * i), tmem + kColS + 128u * i + 32u * x,
-                                    vd + (uint64_t)((stage * L::kTile + x * 64 * 128) >> 4), id_o, !first || x > 0);
+                                    vd + (uint32_t)((stage * L::kTile + x * 64 * 128) >> 4), id_o, !first || x > 0);
                 };
-                if (ok && steps > 0) {
+                if (ok) {
                     const uint32_t s0 = step_at;
                     ok = wait_bounded(&bars.k_full[s0 & 1], (s0 >> 1) & 1, wd, kSiteChunkK, (int)s0);
                     if (ok) {
