@@ -11,7 +11,7 @@
 // exactly, so the only rounding before the output is that of P. Scales are per
 // token: s_K multiplies columns of S, s_V columns of P.
 //
-// Two warpgroups unpack the codes of K and V for both row tiles (each code is
+// One warpgroup unpacks the codes of K and V for both row tiles (each code is
 // unpacked once per 256 rows; c | 0x6400 is the half 1024 + c and c << 4 | 0x5400 is 64 + c,
 // so an AND-OR and a subtraction of 1024 + z or 64 + z give two codes), one
 // thread issues the products, two warpgroups do the softmaxes, in turn with
@@ -44,12 +44,12 @@ namespace {
 constexpr int kChCtas = 148;         // one per SM
 constexpr int kChKeys = 128;         // keys per step
 constexpr int kChRows = 256;         // rows per item: two tiles of 128
-constexpr int kChThreads = 640;      // warpgroups: softmax 0 and 1, unpack K, unpack V, issue (one of its warps)
+constexpr int kChThreads = 512;      // warpgroups: softmax 0 and 1, unpack, issue (one of its warps)
 constexpr int kChSlots = 2 * kChCtas;   // pieces of divided items
 constexpr int kChOverhead = 3;       // cost of a piece beside its steps, in steps
-// Registers per thread: the pool is 640 threads x 96, of which the roles take
-// 256 x 128 + 256 x 88 + 128 x 40 = 60416 of 61440.
-constexpr int kRegsSoftmax = 128, kRegsUnpack = 88, kRegsIssue = 40;
+// Registers per thread: the pool is 512 threads x 128, of which the roles take
+// 256 x 184 + 128 x 104 + 128 x 40 = 65536.
+constexpr int kRegsSoftmax = 184, kRegsUnpack = 104, kRegsIssue = 40;
 constexpr float kChSlack = 6.0f;     // log2 by which scores may exceed the running maximum
 constexpr int kDvThreads = 1024;
 
@@ -57,7 +57,8 @@ struct ChunkParams {
     PagedAttnParams a;
     int rows_limit;      // requests with at most so many (row, head) pairs per KV head belong to the few-rows kernel
     int slot_rows;       // rows of a partial result
-    int32_t *division;   // start[B + 1], slot[B + 1], parts[B]: pieces before, divided pieces before, parts per item
+    int32_t *division;   // by place in the order: start[B + 1], slot[B + 1] (pieces and divided pieces before),
+                         // parts[B] (per item), request[B]
     int32_t *slots;      // [kChSlots][4]: request, head, tile, parts of the item whose part 0 the slot holds (else parts 0)
     float *part;         // [kChSlots][slot_rows][D] outputs, then [kChSlots][slot_rows][2] (maximum, sum)
 };
@@ -122,8 +123,14 @@ __device__ __forceinline__ int64_t block_sum64(int64_t v, int64_t *red) {
 // How the batch is divided, by one CTA. Undivided, the items run in
 // ceil(items / SMs) rounds of their average length; cut into parts of at most S
 // steps they run in more rounds of shorter parts. The cheapest of a few S is
-// taken, among those whose divided pieces fit the slots.
+// taken, among those whose divided pieces fit the slots. Requests are taken
+// in the order of their longest items, so that the pieces' lengths fall along
+// the list, which goes round the CTAs forth and back (32 requests of 1500 to 4500
+// tokens: 166 us with the order given, see below for what it costs without).
+constexpr int kSortBatch = 2048;   // largest batch that is ordered; larger ones have short items enough
+
 __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __grid_constant__ ChunkParams w) {
+    __shared__ int order_s[kSortBatch], key_s[kSortBatch];
     __shared__ int64_t red[32];
     __shared__ int red0[32], red1[32];
     const PagedAttnParams &p = w.a;
@@ -160,11 +167,28 @@ __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __
             if (cut <= kChSlots && cost < best) best = cost, S = x;
         }
     }
+    const bool sorted = p.B <= kSortBatch;
+    if (sorted) {
+        for (int b = threadIdx.x; b < p.B; b += kDvThreads) {
+            int k, hi, lo;
+            chunk_request(w, b, k, hi, lo);
+            key_s[b] = hi;
+        }
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += kDvThreads) {
+            const int mine = key_s[b];
+            int rank = 0;
+            for (int x = 0; x < p.B; ++x) rank += key_s[x] > mine || (key_s[x] == mine && x < b);
+            order_s[rank] = b;
+        }
+        __syncthreads();
+    }
     int base0 = 0, base1 = 0;
     for (int b0 = 0; b0 < p.B; b0 += kDvThreads) {
-        const int b = b0 + threadIdx.x;
+        const int b = b0 + threadIdx.x;   // place in the order
+        const int request = b < p.B ? (sorted ? order_s[b] : b) : 0;
         int k = 0, hi = 0, lo = 0;
-        if (b < p.B) chunk_request(w, b, k, hi, lo);
+        if (b < p.B) chunk_request(w, request, k, hi, lo);
         const int parts = max(1, (int)((hi + S - 1) / S));
         const int v0 = k * parts, v1 = parts > 1 ? v0 : 0;
         int i0 = v0, i1 = v1;
@@ -185,6 +209,7 @@ __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __
             w.division[b] = o0 + i0 - v0;
             w.division[p.B + 1 + b] = o1 + i1 - v1;
             w.division[2 * p.B + 2 + b] = parts;
+            w.division[3 * p.B + 2 + b] = request;
         }
     }
     if (threadIdx.x == 0) w.division[p.B] = base0, w.division[2 * p.B + 1] = base1;
@@ -276,12 +301,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// The accesses below are warp-collective: the warp must be converged.
+//
 // Loads of 16 lanes x 32 columns in the layout of matrix fragments: lane t's
 // registers 4 j .. 4 j + 3 are row t / 4, columns 8 j + 2 (t % 4) and the next
 // one, and the same of row t / 4 + 8. Without the wait: tmem_wait16 must come
 // before any use of r.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
-    __syncwarp();   // warp-collective (.sync.aligned)
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -298,7 +324,6 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
 
 // The store that matches tmem_ld_frag, without its wait.
 __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[16]) {
-    __syncwarp();   // warp-collective (.sync.aligned)
     asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
@@ -307,7 +332,6 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)
 // 16 lanes x 16 columns of FP16 pairs: register 2 j is row t / 4, column 4 j + t % 4,
 // register 2 j + 1 the same of row t / 4 + 8. Without the wait.
 __device__ __forceinline__ void tmem_st_half_frag(uint32_t taddr, const uint32_t (&r)[8]) {
-    __syncwarp();   // warp-collective (.sync.aligned)
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
@@ -579,6 +603,7 @@ __device__ __forceinline__ void softmax_rows(uint32_t ts, uint32_t kf, uint32_t 
                 for (int j = 0; j < 4; ++j)
                     b.x[i >> 1][2 * j + (i & 1)] = add2(b.x[i >> 1][2 * j + (i & 1)], pair_of(-up, -up));
             }
+            __syncwarp();
             // The step's weights stored so far.
 #pragma unroll 1
             for (int o = 0; o < q; ++o)
@@ -632,7 +657,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         mbar_init(&bars.drain, 1);
         mbar_fence_init();
     }
-    if (warp == 16) {
+    if (warp == 12) {
         tmem_alloc(&tmem_s, 512);
         tmem_relinquish();
     }
@@ -657,16 +682,16 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     auto locate = [&](int round, ChunkPiece *out) {
         const int piece = round * (int)gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
         if (__any_sync(0xffffffffu, piece >= pieces || abort_s != 0)) return false;
-        int lo = 0, hi = p.B - 1;   // the last request that starts at or before the piece
+        int lo = 0, hi = p.B - 1;   // the last place that starts at or before the piece
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (w.division[mid] <= piece) lo = mid;
             else hi = mid - 1;
         }
         ChunkPiece c;
-        c.b = lo;
+        c.b = w.division[3 * p.B + 2 + lo];
         c.parts = w.division[2 * p.B + 2 + lo];
-        c.r = paged_request(p, lo);
+        c.r = paged_request(p, c.b);
         const int rest = piece - w.division[lo], tiles = (c.r.n * p.G + kChRows - 1) / kChRows;
         // Long items first: the last tile's parts of every head, then the tile before.
         const int per_tile = c.parts * p.Hkv;
@@ -850,12 +875,10 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             }
             tc_fence_before();   // the next piece's products come after these reads
         }
-    } else if (wg < 4) {
+    } else if (wg == 2) {
         // ---------------------------------------------------------- unpack
-        // One warpgroup each for K and V, alike: codes to FP16, the
-        // scales to factors of the scores or of the weights.
+        // Codes to FP16, scales to factors of the scores and of the weights.
         regs_dec<kRegsUnpack>();
-        const bool value = wg == 3;
         const int t = tid & 127;
         // A thread unpacks chunk j (16 bytes, 32 dims) of the tokens
         // tk + 128 / CPT i: two lanes read a 32-byte half of a token's codes,
@@ -866,16 +889,14 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         const int page_mask = (1 << p.page_shift) - 1;
         const uint32_t page_vecs = (uint32_t)p.Hkv << p.page_shift, page_bytes = page_vecs * DB;
         const uint32_t last_page = (uint32_t)p.n_pages - 1u;
-        const uint8_t *codes = value ? p.v_codes : p.k_codes;
-        const uint32_t *params = reinterpret_cast<const uint32_t *>(value ? p.v_params : p.k_params);
-        const uint32_t zeros = base + (uint32_t)(L::kZ + (value ? 4 * 2 * kChKeys : 0));
-        uint64_t *full = value ? bars.v_full : bars.k_full, *empty = value ? bars.v_free : bars.k_free;
-        // Where the thread's four groups of 8 dims of its first token go.
+        const int64_t v_minus_k = p.v_codes - p.k_codes;
+        const uint32_t zeros = base + (uint32_t)L::kZ;
+        // Where the thread's four groups of 8 dims of its first token go, in K's
+        // first stage.
         uint32_t to[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-            to[x] = base + (uint32_t)((value ? L::kV : L::kK) + tk * 128 + (j >> 1) * L::kPanel +
-                                      (((4 * (j & 1) + x) ^ (tk & 7)) << 4));
+            to[x] = base + (uint32_t)(L::kK + tk * 128 + (j >> 1) * L::kPanel + (((4 * (j & 1) + x) ^ (tk & 7)) << 4));
         // Steps start at multiples of 128 tokens, so a token's place within
         // its page and its table entry relative to the step's first do not
         // change from step to step (pages of 256 tokens: but for 128).
@@ -884,16 +905,16 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         for (int i = 0; i < CPL; ++i) part[i] = (tk + i * kStride) >> p.page_shift;
         const int part_t = t >> p.page_shift;   // of token t
         walk([&](const ChunkPiece &pc) {
-            const PagedRequest &r = pc.r;
-            const int b = pc.b, k0 = pc.k0, k1 = pc.k1;
-            const int32_t *table = p.block_table + (int64_t)b * p.max_pages;
-            const int last_entry = (r.kv - 1) >> p.page_shift;   // there is a step only where r.kv > 0
+            const int k0 = pc.k0, k1 = pc.k1, kv = pc.r.kv;
+            if (k0 == k1) return;
+            const int32_t *table = p.block_table + (int64_t)pc.b * p.max_pages;
+            const int last_entry = (kv - 1) >> p.page_shift;   // there is a step only where kv > 0
             const uint32_t head_vec = (uint32_t)pc.h << p.page_shift;
-            const uint8_t *from[CPL];   // the chunks' places in page 0
+            const uint8_t *from[CPL];   // the chunks' places in page 0 of K
 #pragma unroll
             for (int i = 0; i < CPL; ++i)
-                from[i] = codes + ((uint64_t)head_vec + ((tk + i * kStride) & page_mask)) * DB + j * 16;
-            const uint32_t *from_t = params + head_vec + (t & page_mask);
+                from[i] = p.k_codes + ((uint64_t)head_vec + ((tk + i * kStride) & page_mask)) * DB + j * 16;
+            const int64_t from_t = (int64_t)head_vec + (t & page_mask);
             // Table entries are loaded a step before anything depends on them.
             struct Pages {
                 int chunk[CPL], token;
@@ -906,102 +927,110 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             };
             // Step k's codes of this thread. Numbers outside the cache read
             // its last page, which scales of 0 make nothing of.
-            auto load_codes = [&](int k, const Pages &g, uint4 (&u)[CPL]) {
-                const uint32_t more = p.page_shift == 8 ? (uint32_t)(key_of(pc.st, min(k, k1 - 1)) & 128) * DB : 0u;
+            auto load_codes = [&](int k, const Pages &g, int64_t tensor, uint4 (&u)[CPL]) {
+                const int64_t more = tensor + (p.page_shift == 8 ? (key_of(pc.st, min(k, k1 - 1)) & 128) * DB : 0);
 #pragma unroll
                 for (int i = 0; i < CPL; ++i)
                     u[i] = __ldg(reinterpret_cast<const uint4 *>(
                         from[i] + (uint64_t)min((uint32_t)g.chunk[i], last_page) * page_bytes + more));
             };
-            auto load_sz = [&](int k, int page) {   // token t's scale and zero
-                uint32_t sz = 0u;
+            uint32_t szk = 0u, szv = 0u;   // token t's scales and zeros
+            auto load_sz = [&](int k, int page) {
+                szk = szv = 0u;
                 const int key = key_of(pc.st, k) + t;
-                if (k < k1 && key < r.kv) {
-                    if ((uint32_t)page <= last_page)
-                        sz = __ldg(from_t + (uint64_t)(uint32_t)page * page_vecs + (p.page_shift == 8 ? (key - t) & 128 : 0));
-                    else
-                        paged_bad_request(p, b);
+                if (k < k1 && key < kv) {
+                    if ((uint32_t)page <= last_page) {
+                        const int64_t at = from_t + (int64_t)page * page_vecs + (p.page_shift == 8 ? (key - t) & 128 : 0);
+                        szk = __ldg(reinterpret_cast<const uint32_t *>(p.k_params) + at);
+                        szv = __ldg(reinterpret_cast<const uint32_t *>(p.v_params) + at);
+                    } else {
+                        paged_bad_request(p, pc.b);
+                    }
                 }
-                return sz;
             };
-            if (k0 == k1) return;
-            uint4 u[CPL], un[CPL];   // codes of this step and the next
-            Pages g;                 // entries of the next step
+            uint4 uk[CPL], uv[CPL];   // this step's codes, then the next one's
+            Pages g;                  // entries of the next step
             load_pages(k0, g);
-            load_codes(k0, g, u);
-            uint32_t sz = load_sz(k0, g.token);
+            load_codes(k0, g, 0, uk);
+            load_codes(k0, g, v_minus_k, uv);
+            load_sz(k0, g.token);
             load_pages(k0 + 1, g);
             int eb = 103;   // 127 + the exponent of the largest value scale so far (scales >= 2^-24)
             bool ok = true;
+            // A tensor's tile into its stage at `place` past K's first.
+            auto unpack_tile = [&](const uint4 (&u)[CPL], uint32_t z, uint32_t place) {
+                uint32_t dst[4], zz[CPL];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) dst[x] = to[x] + place;
+#pragma unroll
+                for (int i = 0; i < CPL; ++i) zz[i] = lds32(z + 4 * (tk + i * kStride));   // halves 1024 + z, 64 + z
+                auto unpack = [&](auto index) {
+                    constexpr int i = decltype(index)::value;
+                    const uint32_t z1 = __byte_perm(zz[i], zz[i], 0x1010), z2 = __byte_perm(zz[i], zz[i], 0x3232);
+                    const uint32_t words[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t c = words[x], c8 = c >> 8;
+                        sts128_at<i * kStride * 128>(
+                            dst[x], hsub2((c & 0x000F000Fu) | 0x64006400u, z1), hsub2((c & 0x00F000F0u) | 0x54005400u, z2),
+                            hsub2((c8 & 0x000F000Fu) | 0x64006400u, z1), hsub2((c8 & 0x00F000F0u) | 0x54005400u, z2));
+                    }
+                };
+                unpack(Index<0>());
+                unpack(Index<1>());
+                if constexpr (CPL == 4) {
+                    unpack(Index<2>());
+                    unpack(Index<3>());
+                }
+                fence_proxy_async_smem();
+            };
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
                 const uint32_t s = step_at + (uint32_t)(k - k0), stage = s & 1;
-                const uint32_t z = zeros + 4 * stage * kChKeys;
+                const uint32_t z = zeros + 4 * stage * 2 * kChKeys;
                 // The step's factors. A written scale is finite and a zero at
                 // most 15; the bounds make a hidden token's values
                 // so too, whatever it holds, so that its weight 0 stays 0.
-                const uint32_t scale = value ? min(sz & 0xFFFFu, 0x7BFFu) : sz & 0xFFFFu;
-                const float zero = fminf(fmaxf(__half2float(half_hi(sz)), 0.0f), 15.0f);
-                sts32(z + 4 * t, half2_bits(__floats2half2_rn(1024.0f + zero, 64.0f + zero)));
-                if (value) {
-                    const uint32_t wmax = __reduce_max_sync(0xffffffffu, scale);
-                    if (lane == 0) emax_s[stage][warp & 3] = wmax;
-                }
+                const uint32_t sv = min(szv & 0xFFFFu, 0x7BFFu);
+                const float zk = fminf(fmaxf(__half2float(half_hi(szk)), 0.0f), 15.0f);
+                const float zv = fminf(fmaxf(__half2float(half_hi(szv)), 0.0f), 15.0f);
+                sts32(z + 4 * t, half2_bits(__floats2half2_rn(1024.0f + zk, 64.0f + zk)));
+                sts32(z + 4 * (kChKeys + t), half2_bits(__floats2half2_rn(1024.0f + zv, 64.0f + zv)));
+                const uint32_t wmax = __reduce_max_sync(0xffffffffu, sv);
+                if (lane == 0) emax_s[stage][warp & 3] = wmax;
                 // The only meeting of a step: zeros and maxima are double-buffered.
-                if (named_bar_any(2 + (value ? 1 : 0), 128, !ok)) break;
+                if (named_bar_any(2, 128, !ok)) break;
                 const uint32_t f = factors + 4 * ((s & 3) * 2 * kChKeys + t);
-                if (value) {
-                    const uint32_t top = max(max(emax_s[stage][0], emax_s[stage][1]), max(emax_s[stage][2], emax_s[stage][3]));
-                    const int ebn = max(eb, (int)(__float_as_uint(half_lo(top)) >> 23));
-                    sts32f(f + 4 * kChKeys, half_lo(scale) * __int_as_float((262 - ebn) << 23));   // 2^(8 - E)
-                    if (t == 0) {
-                        es_s[s & 3] = __int_as_float((127 + eb - ebn) << 23);
-                        unit_s[s & 3] = __int_as_float((ebn - 8) << 23);
-                    }
-                    eb = ebn;
-                } else {
-                    sts32f(f, half_lo(scale) * p.qscale);
+                const uint32_t top = max(max(emax_s[stage][0], emax_s[stage][1]), max(emax_s[stage][2], emax_s[stage][3]));
+                const int ebn = max(eb, (int)(__float_as_uint(half_lo(top)) >> 23));
+                sts32f(f, half_lo(szk) * p.qscale);
+                sts32f(f + 4 * kChKeys, half_lo(sv) * __int_as_float((262 - ebn) << 23));   // 2^(8 - E)
+                if (t == 0) {
+                    es_s[s & 3] = __int_as_float((127 + eb - ebn) << 23);
+                    unit_s[s & 3] = __int_as_float((ebn - 8) << 23);
                 }
-                sz = load_sz(k + 1, g.token);
-                load_codes(k + 1, g, un);
-                load_pages(k + 2, g);
-                uint32_t zz[CPL];
-#pragma unroll
-                for (int i = 0; i < CPL; ++i) zz[i] = lds32(z + 4 * (tk + i * kStride));   // halves 1024 + z, 64 + z
-                ok = s < 2 || wait_long(&empty[stage], ((s >> 1) - 1) & 1, wd, kSiteChunkFree, (int)s);
+                eb = ebn;
+                load_sz(k + 1, g.token);
+                const uint32_t freed = ((s >> 1) - 1) & 1;
+                ok = s < 2 || wait_long(&bars.k_free[stage], freed, wd, kSiteChunkFree, (int)s);
                 if (ok) {
-                    uint32_t dst[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) dst[x] = to[x] + stage * (uint32_t)L::kTile;
-                    auto unpack = [&](auto index) {
-                        constexpr int i = decltype(index)::value;
-                        const uint32_t z1 = __byte_perm(zz[i], zz[i], 0x1010), z2 = __byte_perm(zz[i], zz[i], 0x3232);
-                        const uint32_t words[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t c = words[x], c8 = c >> 8;
-                            sts128_at<i * kStride * 128>(
-                                dst[x], hsub2((c & 0x000F000Fu) | 0x64006400u, z1), hsub2((c & 0x00F000F0u) | 0x54005400u, z2),
-                                hsub2((c8 & 0x000F000Fu) | 0x64006400u, z1), hsub2((c8 & 0x00F000F0u) | 0x54005400u, z2));
-                        }
-                    };
-                    unpack(Index<0>());
-                    unpack(Index<1>());
-                    if constexpr (CPL == 4) {
-                        unpack(Index<2>());
-                        unpack(Index<3>());
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&full[stage]);
+                    unpack_tile(uk, z, stage * (uint32_t)L::kTile);
+                    mbar_arrive(&bars.k_full[stage]);
                 }
-#pragma unroll
-                for (int i = 0; i < CPL; ++i) u[i] = un[i];
+                load_codes(k + 1, g, 0, uk);
+                ok = ok && (s < 2 || wait_long(&bars.v_free[stage], freed, wd, kSiteChunkFree, (int)s));
+                if (ok) {
+                    unpack_tile(uv, z + 4 * kChKeys, (uint32_t)(L::kV - L::kK) + stage * (uint32_t)L::kTile);
+                    mbar_arrive(&bars.v_full[stage]);
+                }
+                load_codes(k + 1, g, v_minus_k, uv);
+                load_pages(k + 2, g);
             }
         });
     } else {
         // ---------------------------------------------------------- issue
         regs_dec<kRegsIssue>();
-        if (warp == 16) walk([&](const ChunkPiece &c) {
+        if (warp == 12) walk([&](const ChunkPiece &c) {
             const int steps = c.k1 - c.k0;
             const bool two = c.rows > 128;
             constexpr uint32_t id_s = idesc_f16(128, kChKeys, false), id_o = idesc_f16(128, D, true);
@@ -1071,7 +1100,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 16) tmem_dealloc(tmem, 512);
+    if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -1137,7 +1166,7 @@ cudaError_t launch(const ChunkParams &w, cudaStream_t stream) {
 
 // Workspace: the division, the slots' items, the partial results.
 size_t chunk_workspace_bytes(int64_t B, int64_t max_new, int64_t G, int64_t D) {
-    return (size_t)align256(4 * (3 * B + 2)) + (size_t)align256(16 * kChSlots) +
+    return (size_t)align256(4 * (4 * B + 2)) + (size_t)align256(16 * kChSlots) +
            (size_t)align256((int64_t)4 * kChSlots * slot_rows(max_new, G) * (D + 2));
 }
 
@@ -1150,7 +1179,7 @@ cudaError_t launch_paged_chunk(const PagedAttnParams &p, int64_t D, int rows_lim
     w.slot_rows = slot_rows(max_new, p.G);
     uint8_t *at = static_cast<uint8_t *>(ws);
     w.division = reinterpret_cast<int32_t *>(at);
-    at += align256(4 * (3 * (int64_t)p.B + 2));
+    at += align256(4 * (4 * (int64_t)p.B + 2));
     w.slots = reinterpret_cast<int32_t *>(at);
     at += align256(16 * kChSlots);
     w.part = reinterpret_cast<float *>(at);
