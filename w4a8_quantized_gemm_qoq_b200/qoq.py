@@ -348,52 +348,85 @@ def kv4_decode_attention(q, kcache, vcache, seq_lens=None, ws=None, out=None, st
 
 
 # ------------------------------------------------------------------ paged KV4
+#
+# A serving step makes these calls for every layer, so their checks are kept
+# short: one test of what a correct argument has, and the reason only where it
+# fails; pointers of the buffers that an object owns are kept with it.
 
-def _device_scope(t):
-    """Launches go to the device of the tensors: a no-op when it is current."""
+_vp, _i64 = ctypes.c_void_p, ctypes.c_int64
+
+
+def _device_scope(device):
+    """Launches go to the tensors' device: entered only when it is not current."""
     import torch
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+    return torch.cuda.device(device)
 
 
-def _i32_buffer(t, shape, like, name):
-    """An int32 CUDA tensor of this shape on the device of `like`."""
+def _current(index):
     import torch
-    t = _cuda_tensor(t, torch.int32, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, like.device))
-    return t
+    return torch._C._cuda_getDevice() == index
 
 
-def _rows(t, name, D=None):
-    """FP16 [N][heads][D] with dense heads and any row stride; returns the row
-    stride in elements."""
+def _raw_stream(stream, index):
+    """The stream to launch on: the given one, or the device's current one."""
     import torch
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+    return _vp(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+
+
+def _stream_scope(stream):
+    """Allocations belong to the stream that uses them."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _i32(t, shape, device, name):
+    """Pointer of an int32 CUDA tensor of this shape on this device."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        _cuda_tensor(t, torch.int32, name)
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    return _vp(t.data_ptr())
+
+
+def _rows(t, heads, D, device, name):
+    """Pointer and row stride (in elements) of FP16 [N][heads][D] with dense heads
+    and any row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError("%s must be %s, got %s" % (name, torch.float16, t.dtype))
-    if t.dim() != 3 or (D is not None and t.shape[2] != D):
-        raise ValueError("%s must have shape [N][heads][%s]" % (name, "D" if D is None else D))
-    n, h, d = t.shape
-    if n and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError("%s must have shape [N][%d][%d], got %s" % (name, heads, D, tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    n = t.shape[0]
+    s = t.stride()
+    if n and (s[2] != 1 or (heads > 1 and s[1] != D)):
         raise ValueError("the heads of a row of %s must be dense" % name)
-    return t.stride(0) if n > 1 else h * d
+    return _vp(t.data_ptr()), s[0] if n > 1 else heads * D
 
 
 class PagedStep:
     """What one step of up to max_tokens rows needs of the page tables
     (include/qoq.h, qoq_kv4_pages_assign): q_start [B + 1], and positions and
-    slots [max_tokens], -1 past the step's rows."""
+    slots [max_tokens], -1 past the step's rows. The buffers stay the same
+    ones, so that a captured step can refer to them."""
 
     def __init__(self, B, max_tokens, device="cuda"):
         import torch
-        self.q_start = torch.zeros((B + 1,), dtype=torch.int32, device=device)
-        self.positions = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
-        self.slots = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
+        self._q_start = torch.zeros((B + 1,), dtype=torch.int32, device=device)
+        self._positions = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
+        self._slots = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
+        self._ptrs = tuple(_vp(t.data_ptr()) for t in (self._q_start, self._positions, self._slots))
+        self.B, self.max_tokens, self.device = B, max_tokens, self._q_start.device
+
+    q_start = property(lambda self: self._q_start)
+    positions = property(lambda self: self._positions)
+    slots = property(lambda self: self._slots)
 
 
 class PageTable:
@@ -416,45 +449,63 @@ class PageTable:
 
     def _set(self, seq_lens, block_table, free_pages, free_count, page_size):
         import torch
-        self.seq_lens = _cuda_tensor(seq_lens, torch.int32, "seq_lens")
+        _cuda_tensor(seq_lens, torch.int32, "seq_lens")
         if seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
             raise ValueError("seq_lens [B], block_table [B][max_pages] and free_pages [n_pages] are expected")
-        self.B = seq_lens.shape[0]
-        self.block_table = _i32_buffer(block_table, (self.B, block_table.shape[1]), seq_lens, "block_table")
-        self.free_pages = _i32_buffer(free_pages, free_pages.shape, seq_lens, "free_pages")
-        self.free_count = _i32_buffer(free_count, (1,), seq_lens, "free_count")
-        self.page_size = int(page_size)
-        self.status_words = torch.zeros((4,), dtype=torch.int32, device=seq_lens.device)
+        B, device = seq_lens.shape[0], seq_lens.device
+        self.B, self.device, self.page_size = B, device, int(page_size)
+        self._seq_lens, self._block_table, self._free_pages, self._free_count = \
+            seq_lens, block_table, free_pages, free_count
+        self.status_words = torch.zeros((4,), dtype=torch.int32, device=device)
+        self._seq = _i32(seq_lens, (B,), device, "seq_lens")
+        self._table = _i32(block_table, (B, block_table.shape[1]), device, "block_table")
+        self._free = _i32(free_pages, free_pages.shape, device, "free_pages")
+        self._count = _i32(free_count, (1,), device, "free_count")
+        self._status = _vp(self.status_words.data_ptr())
+        self._sizes = _i64(B), _i64(self.page_size), _i64(free_pages.shape[0]), _i64(block_table.shape[1])
+
+    seq_lens = property(lambda self: self._seq_lens)
+    block_table = property(lambda self: self._block_table)
+    free_pages = property(lambda self: self._free_pages)
+    free_count = property(lambda self: self._free_count)
 
     def assign(self, new_lens, step, kv_lens=None, free_left=None, stream=None):
         """Begin a step in which new_lens[b] tokens join request b: fills
         `step` and enters the pages taken. The lengths and the free count
         are updated in place, unless kv_lens [B] and free_left [1] are given
         to take the new ones. Returns `step`."""
-        s = self.seq_lens
-        new_lens = _i32_buffer(new_lens, (self.B,), s, "new_lens")
-        _i32_buffer(step.q_start, (self.B + 1,), s, "step.q_start")
-        n = step.slots.shape[0]
-        kv_lens = s if kv_lens is None else _i32_buffer(kv_lens, (self.B,), s, "kv_lens")
-        free_left = self.free_count if free_left is None else _i32_buffer(free_left, (1,), s, "free_left")
-        with _device_scope(s):
-            _check("qoq_kv4_pages_assign", lib().qoq_kv4_pages_assign(
-                _ptr(s), _ptr(new_lens), self.B, self.page_size, _ptr(self.free_pages), _ptr(self.free_count),
-                self.free_pages.shape[0], _ptr(self.block_table), self.block_table.shape[1], n, _ptr(kv_lens),
-                _ptr(step.q_start), _ptr(step.positions), _ptr(step.slots), _ptr(free_left), _ptr(self.status_words),
-                _stream(stream)))
+        device = self.device
+        if not _current(device.index):
+            with _device_scope(device):
+                return self.assign(new_lens, step, kv_lens, free_left, stream)
+        B, page_size, n_pages, max_pages = self._sizes
+        if step.B != self.B or step.device != device:
+            raise ValueError("the step is for %d requests on %s, the table for %d on %s"
+                             % (step.B, step.device, self.B, device))
+        q_start, positions, slots = step._ptrs
+        code = lib().qoq_kv4_pages_assign(
+            self._seq, _i32(new_lens, (self.B,), device, "new_lens"), B, page_size, self._free, self._count, n_pages,
+            self._table, max_pages, step.max_tokens,
+            self._seq if kv_lens is None else _i32(kv_lens, (self.B,), device, "kv_lens"), q_start, positions, slots,
+            self._count if free_left is None else _i32(free_left, (1,), device, "free_left"), self._status,
+            _raw_stream(stream, device.index))
+        if code:
+            _check("qoq_kv4_pages_assign", code)
         return step
 
     def release(self, leave, stream=None):
         """End the requests b with leave[b] != 0 (int32 [B]): their pages are
         free again, their lengths 0."""
-        s = self.seq_lens
-        leave = _i32_buffer(leave, (self.B,), s, "leave")
-        with _device_scope(s):
-            _check("qoq_kv4_pages_release", lib().qoq_kv4_pages_release(
-                _ptr(leave), self.B, self.page_size, _ptr(s), _ptr(self.block_table), self.block_table.shape[1],
-                _ptr(self.free_pages), _ptr(self.free_count), self.free_pages.shape[0], _ptr(self.status_words),
-                _stream(stream)))
+        device = self.device
+        if not _current(device.index):
+            with _device_scope(device):
+                return self.release(leave, stream)
+        B, page_size, n_pages, max_pages = self._sizes
+        code = lib().qoq_kv4_pages_release(_i32(leave, (self.B,), device, "leave"), B, page_size, self._seq, self._table,
+                                           max_pages, self._free, self._count, n_pages, self._status,
+                                           _raw_stream(stream, device.index))
+        if code:
+            _check("qoq_kv4_pages_release", code)
 
     def status(self) -> int:
         """The first refused step's status code (synchronises), 0 if none was."""
@@ -491,55 +542,62 @@ class PagedKV4Cache:
         if k_codes.dim() != 4:
             raise ValueError("k_codes must have shape [n_pages][Hkv][page_size][D/2]")
         n, h, P, db = k_codes.shape
-        if tuple(v_codes.shape) != (n, h, P, db) or tuple(k_params.shape) != (n, h, P, 2) or \
-                tuple(v_params.shape) != (n, h, P, 2):
+        if v_codes.shape != (n, h, P, db) or k_params.shape != (n, h, P, 2) or v_params.shape != (n, h, P, 2):
             raise ValueError("the shapes of codes and params do not match")
         if len({t.device for t in (k_codes, k_params, v_codes, v_params)}) != 1:
             raise ValueError("codes and params must be on one device")
-        self.n_pages, self.Hkv, self.page_size, self.D = n, h, P, 2 * db
-        self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
-        self._ptrs = tuple(_ptr(t) for t in (k_codes, k_params, v_codes, v_params))
+        self.n_pages, self.Hkv, self.page_size, self.D, self.device = n, h, P, 2 * db, k_codes.device
+        self._tensors = k_codes, k_params, v_codes, v_params
+        self._ptrs = tuple(_vp(t.data_ptr()) for t in self._tensors)
+        self._sizes = _i64(h), _i64(2 * db), _i64(n), _i64(P)
+
+    k_codes = property(lambda self: self._tensors[0])
+    k_params = property(lambda self: self._tensors[1])
+    v_codes = property(lambda self: self._tensors[2])
+    v_params = property(lambda self: self._tensors[3])
 
     def write(self, k, v, slots, stream=None):
         """Quantise rows k, v [N][Hkv][D] FP16 (any row stride) into
         slots [N] int32; rows with a slot outside the cache are skipped."""
-        ks, vs = _rows(k, "k", self.D), _rows(v, "v", self.D)
+        device = self.device
+        if not _current(device.index):
+            with _device_scope(device):
+                return self.write(k, v, slots, stream)
+        kp, ks = _rows(k, self.Hkv, self.D, device, "k")
+        vp, vs = _rows(v, self.Hkv, self.D, device, "v")
         N = k.shape[0]
-        if k.shape[1] != self.Hkv or v.shape != k.shape:
-            raise ValueError("k %s and v %s do not match the cache" % (tuple(k.shape), tuple(v.shape)))
-        slots = _i32_buffer(slots, (N,), self.k_codes, "slots")
-        if k.device != slots.device or v.device != slots.device:
-            raise ValueError("k and v must be on the cache's device")
-        with _device_scope(self.k_codes):
-            _check("qoq_kv4_paged_write", lib().qoq_kv4_paged_write(
-                _ptr(k), ks, _ptr(v), vs, _ptr(slots), N, self.Hkv, self.D, self.n_pages, self.page_size,
-                *self._ptrs, _stream(stream)))
+        if v.shape[0] != N:
+            raise ValueError("k has %d rows, v %d" % (N, v.shape[0]))
+        code = lib().qoq_kv4_paged_write(kp, ks, vp, vs, _i32(slots, (N,), device, "slots"), N, *self._sizes,
+                                         *self._ptrs, _raw_stream(stream, device.index))
+        if code:
+            _check("qoq_kv4_paged_write", code)
         return self
 
     def read(self, slots, k=None, v=None, stream=None):
         """The cached K and V of slots [N] as FP16 [N][Hkv][D] each (a sequence
         moved elsewhere, or handed to a dense kernel); 0 outside the cache."""
         import torch
-        slots = _i32_buffer(slots, (slots.shape[0],), self.k_codes, "slots")
-        shape = (slots.shape[0], self.Hkv, self.D)
-        with _device_scope(self.k_codes):
+        device = self.device
+        if not _current(device.index):
+            with _device_scope(device):
+                return self.read(slots, k, v, stream)
+        N = slots.shape[0]
+        sp = _i32(slots, (N,), device, "slots")
+        shape = (N, self.Hkv, self.D)
+        if k is None or v is None:
             with _stream_scope(stream):
-                k = torch.empty(shape, dtype=torch.float16, device=slots.device) if k is None else k
-                v = torch.empty(shape, dtype=torch.float16, device=slots.device) if v is None else v
-            for t, name in ((k, "k"), (v, "v")):
-                _cuda_tensor(t, torch.float16, name)
-                if tuple(t.shape) != shape or t.device != slots.device:
-                    raise ValueError("%s must have shape %s on %s" % (name, shape, slots.device))
-            _check("qoq_kv4_paged_read", lib().qoq_kv4_paged_read(
-                _ptr(slots), shape[0], self.Hkv, self.D, self.n_pages, self.page_size, *self._ptrs, _ptr(k), _ptr(v),
-                _stream(stream)))
+                k = torch.empty(shape, dtype=torch.float16, device=device) if k is None else k
+                v = torch.empty(shape, dtype=torch.float16, device=device) if v is None else v
+        for t, name in ((k, "k"), (v, "v")):
+            _cuda_tensor(t, torch.float16, name)
+            if t.shape != shape or t.device != device:
+                raise ValueError("%s must have shape %s on %s" % (name, shape, device))
+        code = lib().qoq_kv4_paged_read(sp, N, *self._sizes, *self._ptrs, _vp(k.data_ptr()), _vp(v.data_ptr()),
+                                        _raw_stream(stream, device.index))
+        if code:
+            _check("qoq_kv4_paged_read", code)
         return k, v
-
-
-def _stream_scope(stream):
-    """Allocations belong to the stream that uses them."""
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def kv4_paged_workspace_bytes(B, N, Hq, Hkv, D, max_new) -> int:
@@ -555,30 +613,32 @@ def kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window
     """q [N][Hq][D] FP16 (any row stride): rows q_start[b] .. q_start[b + 1] - 1
     are request b's latest tokens, attending to the kv_lens[b] tokens that
     block_table [B][max_pages] holds of it, causally, and with window > 0 only
-    to the latest `window` of them and the first `sinks`. max_new bounds the rows per request (1 for a decode
-    step). Returns out [N][Hq][D] FP16."""
+    to the latest `window` of them and the first `sinks`. max_new bounds the
+    rows per request (1 for a decode step). Returns out [N][Hq][D] FP16."""
     import torch
-    qs = _rows(q, "q", cache.D)
-    N, Hq, D = q.shape
-    like = cache.k_codes
-    B = block_table.shape[0]
-    _i32_buffer(block_table, (B, block_table.shape[1]), like, "block_table")
-    _i32_buffer(q_start, (B + 1,), like, "q_start")
-    _i32_buffer(kv_lens, (B,), like, "kv_lens")
-    if q.device != like.device:
-        raise ValueError("q is on %s, not on %s" % (q.device, like.device))
-    with _device_scope(like):
+    device = cache.device
+    if not _current(device.index):
+        with _device_scope(device):
+            return kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window, sinks, ws, out, stream)
+    Hkv, D, n_pages, page_size = cache._sizes
+    N, Hq = q.shape[0], q.shape[1]
+    qp, qs = _rows(q, Hq, cache.D, device, "q")
+    B, max_pages = block_table.shape
+    if ws is None or out is None:
         with _stream_scope(stream):
             if ws is None:
-                ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, D, max_new), q.device)
+                ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, cache.D, max_new), device)
             if out is None:
-                out = torch.empty((N, Hq, D), dtype=torch.float16, device=q.device)
-        os_ = _rows(out, "out", D)
-        if out.shape != q.shape or out.device != q.device or ws.buf.device != q.device:
-            raise ValueError("out must have q's shape, out and ws its device")
-        n = ctypes.c_size_t(ws.buf.numel())
-        _check("qoq_kv4_paged_attention", lib().qoq_kv4_paged_attention(
-            _ptr(q), qs, *cache._ptrs, _ptr(block_table), block_table.shape[1], _ptr(q_start), _ptr(kv_lens), B, N,
-            max_new, Hq, cache.Hkv, D, cache.n_pages, cache.page_size, window, sinks, _ptr(out), os_, _ptr(ws.buf),
-            ctypes.byref(n), _stream(stream)))
+                out = torch.empty((N, Hq, cache.D), dtype=torch.float16, device=device)
+    op, os_ = _rows(out, Hq, cache.D, device, "out")
+    if out.shape[0] != N or ws.buf.device != device:
+        raise ValueError("out must have q's shape, and the workspace its device")
+    n = ctypes.c_size_t(ws.buf.numel())
+    code = lib().qoq_kv4_paged_attention(
+        qp, qs, *cache._ptrs, _i32(block_table, (B, max_pages), device, "block_table"), max_pages,
+        _i32(q_start, (B + 1,), device, "q_start"), _i32(kv_lens, (B,), device, "kv_lens"), B, N, max_new, Hq, Hkv, D,
+        n_pages, page_size, window, sinks, op, os_, _vp(ws.buf.data_ptr()), ctypes.byref(n),
+        _raw_stream(stream, device.index))
+    if code:
+        _check("qoq_kv4_paged_attention", code)
     return out
