@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qoq_device.cuh"
 #include "qoq_internal.h"
 
@@ -27,5 +29,21 @@ __device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams &p, 
 __device__ __forceinline__ void paged_bad_request(const PagedAttnParams &p, int b) {
     if (atomicCAS(p.status, 0, QOQ_ERR_INVALID_ARG) == 0) p.status[1] = b;
 }
+
+// Opts a kernel in to more than 48 KB of dynamic shared memory, once per device.
+struct SmemOptIn {
+    std::atomic<uint64_t> done{0};   // devices 0 .. 63, a bit each
+    template <typename Kernel>
+    cudaError_t set(Kernel kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 }  // namespace qoq

@@ -94,103 +94,118 @@ __device__ __forceinline__ ChunkSteps chunk_steps(const PagedAttnParams &p, cons
     return s;
 }
 
-// The longest item of a request, in steps (its last tile sees the most keys,
-// or with a window as many as any), and its items.
-__device__ __forceinline__ void chunk_request(const ChunkParams &w, int b, int &items, int &longest, int &shortest) {
-    const PagedRequest r = paged_request(w.a, b);
-    const int rows = chunk_rows(w, r);
-    const int tiles = (rows + kChRows - 1) / kChRows;
-    items = tiles * w.a.Hkv;
-    longest = shortest = 0;
-    if (tiles) {
-        longest = max(1, chunk_steps(w.a, r, tiles - 1).count);
-        shortest = max(1, min(longest, chunk_steps(w.a, r, 0).count));
-    }
-}
-
-__device__ __forceinline__ int64_t block_sum64(int64_t v, int64_t *red) {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = red[threadIdx.x & 31];
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
-    return t;
-}
-
 // How the batch is divided, by one CTA. Undivided, the items run in
 // ceil(items / SMs) rounds of their average length; cut into parts of at most S
 // steps they run in more rounds of shorter parts. The cheapest of a few S is
 // taken, among those whose divided pieces fit the slots. Requests are taken
 // in the order of their longest items, so that the pieces' lengths fall along
 // the list, which goes round the CTAs forth and back (32 requests of 1500 to 4500
-// tokens: 166 us with the order given, see below for what it costs without).
-constexpr int kSortBatch = 2048;   // largest batch that is ordered; larger ones have short items enough
+// tokens, 5 rows each: 138 us, in the order given 179). The attention kernel
+// waits for this one, so it is kept short: one reading of the lengths, one
+// meeting for all sums.
+constexpr int kSortBatch = 2048;   // largest batch that is ordered
+constexpr int kCandidates = 6;
+
+struct ChunkRequest {
+    int items, longest, shortest;
+};
+
+__device__ __forceinline__ ChunkRequest chunk_request(const ChunkParams &w, int b) {
+    const PagedRequest r = paged_request(w.a, b);
+    if (r.n > w.a.max_new) paged_bad_request(w.a, b);
+    const int rows = chunk_rows(w, r);
+    const int tiles = (rows + kChRows - 1) / kChRows;
+    ChunkRequest c = {tiles * w.a.Hkv, 0, 0};
+    if (tiles) {
+        c.longest = max(1, chunk_steps(w.a, r, tiles - 1).count);
+        c.shortest = max(1, min(c.longest, chunk_steps(w.a, r, 0).count));
+    }
+    return c;
+}
 
 __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __grid_constant__ ChunkParams w) {
     __shared__ int order_s[kSortBatch], key_s[kSortBatch];
-    __shared__ int64_t red[32];
+    __shared__ float items_s[32], steps_s[32];
+    __shared__ float sums_s[2 * kCandidates][32];
     __shared__ int red0[32], red1[32];
     const PagedAttnParams &p = w.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t items = 0, steps = 0;
-    for (int b = threadIdx.x; b < p.B; b += kDvThreads) {
-        int n, hi, lo;
-        chunk_request(w, b, n, hi, lo);
-        items += n;
-        steps += (int64_t)n * (hi + lo) / 2;
-        if (paged_request(p, b).n > p.max_new) paged_bad_request(p, b);
-    }
-    items = block_sum64(items, red);
-    steps = block_sum64(steps, red);
-    int64_t S = INT32_MAX;
-    if (items > 0 && items <= 4 * kChCtas) {
-        int64_t best = (items + kChCtas - 1) / kChCtas * (steps + items * kChOverhead) / items;
-        for (int c = 0; c < 6; ++c) {
-            // Parts of 1 / m of an SM's share, and a little more.
-            const int64_t m = 1 + c / 2, x = (steps + kChCtas * m - 1) / (kChCtas * m) * (c % 2 ? 9 : 8) / 8 + (c % 2);
-            if (x < 1) continue;
-            int64_t n = 0, cut = 0;
-            for (int b = threadIdx.x; b < p.B; b += kDvThreads) {
-                int k, hi, lo;
-                chunk_request(w, b, k, hi, lo);
-                const int64_t parts = (hi + x - 1) / x;
-                n += parts * k;
-                cut += parts > 1 ? parts * k : 0;
-            }
-            n = block_sum64(n, red);
-            cut = block_sum64(cut, red);
-            // A cut piece also writes its rows as FP32 and has them read again.
-            const int64_t cost = (n + kChCtas - 1) / kChCtas * (steps + n * kChOverhead + cut) / n;
-            if (cut <= kChSlots && cost < best) best = cost, S = x;
-        }
-    }
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
+    auto warp_sum = [](float v) {
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+        return v;
+    };
+    // The sums guide a choice and are kept in FP32; the slots' bound below holds
+    // exactly, since whole numbers to 2^24 are exact.
     const bool sorted = p.B <= kSortBatch;
-    if (sorted) {
-        for (int b = threadIdx.x; b < p.B; b += kDvThreads) {
-            int k, hi, lo;
-            chunk_request(w, b, k, hi, lo);
-            key_s[b] = hi;
+    const ChunkRequest mine = (int)threadIdx.x < p.B ? chunk_request(w, threadIdx.x) : ChunkRequest{0, 0, 0};
+    float items = (float)mine.items, steps = 0.5f * (float)mine.items * (float)(mine.longest + mine.shortest);
+    if (sorted && (int)threadIdx.x < p.B) key_s[threadIdx.x] = mine.longest;
+    for (int b = threadIdx.x + blockDim.x; b < p.B; b += blockDim.x) {
+        const ChunkRequest c = chunk_request(w, b);
+        items += (float)c.items;
+        steps += 0.5f * (float)c.items * (float)(c.longest + c.shortest);
+        if (sorted) key_s[b] = c.longest;
+    }
+    items = warp_sum(items);
+    steps = warp_sum(steps);
+    if (lane == 0) items_s[warp] = items, steps_s[warp] = steps;
+    __syncthreads();
+    items = warp_sum(lane < warps ? items_s[lane] : 0.0f);
+    steps = warp_sum(lane < warps ? steps_s[lane] : 0.0f);
+
+    int S = INT32_MAX;
+    if (items > 0.0f && items <= 4.0f * kChCtas) {
+        // Parts of 1 / m of an SM's share, and of a little more.
+        auto candidate = [&](int c) {
+            return max(1, (int)(steps / (float)(kChCtas * (1 + c / 2)) * (c % 2 ? 1.125f : 1.0f)) + 1 + c % 2);
+        };
+        float n[2 * kCandidates];
+#pragma unroll
+        for (int c = 0; c < kCandidates; ++c) n[2 * c] = n[2 * c + 1] = 0.0f;
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const ChunkRequest r = b == (int)threadIdx.x ? mine : chunk_request(w, b);
+#pragma unroll
+            for (int c = 0; c < kCandidates; ++c) {
+                const int x = candidate(c), parts = (r.longest + x - 1) / x;
+                n[2 * c] += (float)parts * (float)r.items;
+                n[2 * c + 1] += parts > 1 ? (float)parts * (float)r.items : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 2 * kCandidates; ++c) {
+            const float v = warp_sum(n[c]);
+            if (lane == 0) sums_s[c][warp] = v;
         }
         __syncthreads();
-        for (int b = threadIdx.x; b < p.B; b += kDvThreads) {
-            const int mine = key_s[b];
+        float best = ceilf(items / kChCtas) * (steps / items + (float)kChOverhead);
+#pragma unroll
+        for (int c = 0; c < kCandidates; ++c) {
+            const float all = warp_sum(lane < warps ? sums_s[2 * c][lane] : 0.0f);
+            const float cut = warp_sum(lane < warps ? sums_s[2 * c + 1][lane] : 0.0f);
+            // A cut piece also writes its rows as FP32 and has them read again.
+            const float cost = ceilf(all / kChCtas) * (steps + all * (float)kChOverhead + cut) / all;
+            if (cut <= (float)kChSlots && cost < best) best = cost, S = candidate(c);
+        }
+    }
+    if (sorted) {
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const int key = key_s[b];
             int rank = 0;
-            for (int x = 0; x < p.B; ++x) rank += key_s[x] > mine || (key_s[x] == mine && x < b);
+            for (int x = 0; x < p.B; ++x) rank += key_s[x] > key || (key_s[x] == key && x < b);
             order_s[rank] = b;
         }
         __syncthreads();
     }
     int base0 = 0, base1 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kDvThreads) {
+    for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;   // place in the order
         const int request = b < p.B ? (sorted ? order_s[b] : b) : 0;
-        int k = 0, hi = 0, lo = 0;
-        if (b < p.B) chunk_request(w, request, k, hi, lo);
-        const int parts = max(1, (int)((hi + S - 1) / S));
-        const int v0 = k * parts, v1 = parts > 1 ? v0 : 0;
+        const ChunkRequest r = b < p.B ? chunk_request(w, request) : ChunkRequest{0, 0, 0};
+        const int parts = S == INT32_MAX ? 1 : max(1, (r.longest + S - 1) / S);
+        const int v0 = r.items * parts, v1 = parts > 1 ? v0 : 0;
         int i0 = v0, i1 = v1;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
@@ -201,7 +216,7 @@ __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __
         if (lane == 31) red0[warp] = i0, red1[warp] = i1;
         __syncthreads();
         int o0 = base0, o1 = base1;
-        for (int x = 0; x < kDvThreads / 32; ++x) {
+        for (int x = 0; x < warps; ++x) {
             if (x < warp) o0 += red0[x], o1 += red1[x];
             base0 += red0[x], base1 += red1[x];
         }
@@ -668,6 +683,8 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     const uint32_t base = (smem_u32(ch_raw) + 1023u) & ~1023u;
     const uint32_t factors = base + (uint32_t)L::kF;
 
+    griddep_wait();   // the division
+    griddep_launch_dependents();
     const int pieces = w.division[p.B];
     // What this CTA's earlier pieces used of each barrier: steps, pieces and
     // pieces with steps, and of each those with a second row tile.
@@ -1107,42 +1124,49 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
 
 namespace {
 
-// Joins the parts of divided items: one warp per row, CTAs over (slot of a
-// part 0, block of rows).
-constexpr int kJoinRows = 16;
+// Joins the parts of divided items, one warp per row.
+constexpr int kJoinRows = 16;   // of an item, per turn of a CTA
+constexpr int kJoinCtas = 8 * kChCtas;
 
 template <int D>
 __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_constant__ ChunkParams w) {
     const PagedAttnParams &p = w.a;
-    const int slot = blockIdx.x;
-    if (slot >= w.division[2 * p.B + 1]) return;
-    const int4 it = *reinterpret_cast<const int4 *>(w.slots + 4 * slot);   // request, head, tile, parts
-    const int parts = it.w;
-    if (parts == 0) return;
-    const PagedRequest r = paged_request(p, it.x);
-    const int rows = min(r.n * p.G - it.z * kChRows, kChRows);
+    griddep_wait();   // the parts
+    const int slots = w.division[2 * p.B + 1], turns = w.slot_rows / kJoinRows;
     const int lane = threadIdx.x & 31;
     const float2 *ml = reinterpret_cast<const float2 *>(w.part + (int64_t)kChSlots * w.slot_rows * D);
-    for (int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5); row < min(rows, (int)(blockIdx.y + 1) * kJoinRows); row += 8) {
-        float m = -INFINITY, l = 0.0f, o[D / 32];
+#pragma unroll 1
+    for (int turn = blockIdx.x; turn < slots * turns; turn += gridDim.x) {
+        const int slot = turn / turns, row0 = (turn - slot * turns) * kJoinRows;
+        const int4 it = *reinterpret_cast<const int4 *>(w.slots + 4 * slot);   // request, head, tile, parts
+        const int parts = it.w;
+        if (parts == 0) continue;   // not an item's first
+        const PagedRequest r = paged_request(p, it.x);
+        const int rows = min(min(r.n * p.G - it.z * kChRows, kChRows), row0 + kJoinRows);
+#pragma unroll 1
+        for (int row = row0 + (threadIdx.x >> 5); row < rows; row += 8) {
+            float m = -INFINITY, l = 0.0f, o[D / 32];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
-        for (int i = 0; i < parts; ++i) m = fmaxf(m, ml[(int64_t)(slot + i) * w.slot_rows + row].x);
-        for (int i = 0; i < parts; ++i) {
-            const int64_t at = (int64_t)(slot + i) * w.slot_rows + row;
-            const float2 x = ml[at];
-            const float f = x.y > 0.0f ? exp2f(x.x - m) : 0.0f;
-            l += f * x.y;
-            const float *src = w.part + at * D + lane * (D / 32);
+            for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < parts; ++i) m = fmaxf(m, ml[(int64_t)(slot + i) * w.slot_rows + row].x);
+#pragma unroll 2
+            for (int i = 0; i < parts; ++i) {
+                const int64_t at = (int64_t)(slot + i) * w.slot_rows + row;
+                const float2 x = ml[at];
+                const float f = x.y > 0.0f ? exp2f(x.x - m) : 0.0f;
+                l += f * x.y;
+                const float *src = w.part + at * D + lane * (D / 32);
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
+                for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
+            }
+            const float f = l > 0.0f ? 1.0f / l : 0.0f;
+            const int pair = it.z * kChRows + row, token = pair / p.G;
+            __half2 *out = reinterpret_cast<__half2 *>(p.out + (int64_t)(r.row0 + token) * p.out_stride +
+                                                       (int64_t)(it.y * p.G + pair - token * p.G) * D + lane * (D / 32));
+#pragma unroll
+            for (int e = 0; e < D / 32; e += 2) out[e / 2] = __floats2half2_rn(o[e] * f, o[e + 1] * f);
         }
-        const float f = l > 0.0f ? 1.0f / l : 0.0f;
-        const int pair = it.z * kChRows + row, token = pair / p.G;
-        __half2 *out = reinterpret_cast<__half2 *>(p.out + (int64_t)(r.row0 + token) * p.out_stride +
-                                                   (int64_t)(it.y * p.G + pair - token * p.G) * D + lane * (D / 32));
-#pragma unroll
-        for (int e = 0; e < D / 32; e += 2) out[e / 2] = __floats2half2_rn(o[e] * f, o[e + 1] * f);
     }
 }
 
@@ -1151,15 +1175,35 @@ int slot_rows(int64_t max_new, int64_t G) {
     return rows >= kChRows ? kChRows : (int)((rows + kJoinRows - 1) / kJoinRows * kJoinRows);
 }
 
+// A launch that may begin before the kernel ahead of it has ended, whose results
+// it waits for itself.
+template <typename Kernel>
+cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, const ChunkParams &w, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, w);
+}
+
 template <int D>
 cudaError_t launch(const ChunkParams &w, cudaStream_t stream) {
     constexpr int smem = ChunkSmem<D>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kv4_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in.set(kv4_chunk_kernel<D>, smem);
     if (e != cudaSuccess) return e;
-    kv4_chunk_division_kernel<<<1, kDvThreads, 0, stream>>>(w);
-    kv4_chunk_kernel<D><<<kChCtas, kChThreads, smem, stream>>>(w);
-    kv4_chunk_join_kernel<D><<<dim3(kChSlots, (unsigned)(w.slot_rows / kJoinRows)), 256, 0, stream>>>(w);
-    return cudaGetLastError();
+    const int threads = w.a.B >= kDvThreads ? kDvThreads : (w.a.B + 31) / 32 * 32;
+    kv4_chunk_division_kernel<<<1, threads, 0, stream>>>(w);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dependent(kv4_chunk_kernel<D>, kChCtas, kChThreads, smem, w, stream);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kv4_chunk_join_kernel<D>, kJoinCtas, 256, 0, w, stream);
 }
 
 }  // namespace

@@ -781,8 +781,8 @@ cudaError_t launch(const RowsParams &w, cudaStream_t stream) {
     // warp): 52 KB at D = 128, four CTAs per SM.
     constexpr int smem = kRwWarps * 3 * kRwTile * D / 2 + kRwWarps * kRwTile * 8 * 2;
     if (smem > 40 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kv4_rows_kernel<D, NSUB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static SmemOptIn opt_in;
+        const cudaError_t e = opt_in.set(kv4_rows_kernel<D, NSUB>, smem);
         if (e != cudaSuccess) return e;
     }
     kv4_rows_kernel<D, NSUB><<<kRwResident, kRwThreads, smem, stream>>>(w);

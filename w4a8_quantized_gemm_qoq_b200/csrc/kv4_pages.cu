@@ -161,19 +161,36 @@ __global__ void __launch_bounds__(kPgThreads) kv4_assign_kernel(const __grid_con
         *p.free_left = code ? count : count - (int)pages;
         if (code) record(p.status, code, request, rows, pages);
     }
-    for (int t = rank * kPgThreads + tid; t < p.max_tokens; t += ctas * kPgThreads) {
-        int pos = -1, slot = -1;
-        if (t < total) {
-            const int b = owner_of(row0, p.B, t);
+    // A row per thread where that covers the step (its loads are independent);
+    // else four in a row, with one search and one table or stack entry per page
+    // (37000 rows of 256 requests: 11 us, 13 with a row per thread).
+    const int per = total <= ctas * kPgThreads ? 1 : 4;
+    const bool wide = per == 4 && ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
+    for (int t = per * (rank * kPgThreads + tid); t < p.max_tokens; t += per * ctas * kPgThreads) {
+        int pos[4], slot[4];
+        int b = t < total ? owner_of(row0, p.B, t) : 0, entry = -1, page = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            pos[e] = slot[e] = -1;
+            if (e >= per || t + e >= total) continue;
+            while (b + 1 < p.B && row0[b + 1] <= t + e) ++b, entry = -1;
             const int s = len[b];
-            pos = s + (t - row0[b]);
-            const int i = pos >> p.page_shift, have = (s + P - 1) >> p.page_shift;
-            const int page = i < have ? p.block_table[(int64_t)b * p.max_pages + i]
-                                      : p.free_pages[count - 1 - page0[b] - (i - have)];
-            slot = (page << p.page_shift) + (pos & (P - 1));
+            pos[e] = s + (t + e - row0[b]);
+            const int i = pos[e] >> p.page_shift, have = (s + P - 1) >> p.page_shift;
+            if (i != entry) {
+                entry = i;
+                page = i < have ? p.block_table[(int64_t)b * p.max_pages + i] : p.free_pages[count - 1 - page0[b] - (i - have)];
+            }
+            slot[e] = (page << p.page_shift) + (pos[e] & (P - 1));
         }
-        p.positions[t] = pos;
-        p.slots[t] = slot;
+        if (wide && t + 4 <= p.max_tokens) {
+            *reinterpret_cast<int4 *>(p.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(p.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < per && t + e < p.max_tokens) p.positions[t + e] = pos[e], p.slots[t + e] = slot[e];
+        }
     }
     if (code == 0)
         for (int g = rank * kPgThreads + tid; g < (int)pages; g += ctas * kPgThreads) {
