@@ -10,9 +10,8 @@ size_t kv4_paged_workspace_bytes(int64_t B, int64_t, int64_t Hq, int64_t Hkv, in
     return 256 + rows_workspace_bytes(B, D) + (max_new * G > kRowsMax ? chunk_workspace_bytes(B, max_new, G, D) : 0);
 }
 
-// A request with at most 8 (row, head) pairs per KV head fits the columns of
-// the few-rows kernel, which reads its cache once at the rate of HBM; the
-// others' products fill the tensor core's 128-row tiles. Where
+// A request with at most 32 (row, head) pairs per KV head goes to the few-rows
+// kernel; the others' products fill the tensor core's 128-row tiles. Where
 // every request has max_new rows (as N says it may) and those are many, the
 // few-rows kernel would find nothing, and the other takes whatever comes.
 cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws,

@@ -1,11 +1,15 @@
 // Paged KV4 attention for requests with few rows: n new tokens x G query
-// heads per KV head <= 8 (decode steps, short drafts).
+// heads per KV head <= 32 (decode steps, short drafts).
 //
 // The work is one pass over the request's K and V codes (D + 8 bytes per
 // token and KV head), so it is bound by HBM where sequences are long, and by
-// a launch's latency where they are short. The n x G (row, head) pairs of a
-// KV head are the 8 columns of the tensor-core products, so K and V are read
-// once for all of them.
+// a launch's latency where they are short. Eight of a KV head's n x G (row,
+// head) pairs are the columns of the tensor-core products, so K and V are read
+// once for all of them; more pairs are columns of further pieces, which read
+// the same cache again (from L2, as they run side by side). That costs 8
+// columns x 64 tokens about 410 cycles of an SM; the many-rows kernel costs up to
+// 128 pairs x 128 tokens about 5000, so up to 32 pairs come here (32 sequences
+// x 5 rows x 4 heads: FIG us here, 127 there).
 //
 // Pieces. The lengths are known on the device only, so every CTA works out the
 // same division: a request's visible tokens are 64-token tiles (those of the
@@ -57,15 +61,15 @@ constexpr int kRwWarps = 4;
 constexpr int kRwThreads = 32 * kRwWarps;
 constexpr int kRwTile = 64;                   // tokens per warp tile
 constexpr int kRwResident = 4 * 148;          // CTAs that run at once
-constexpr int kRwSplitSlots = 2 * kRwResident;   // pieces of divided (request, head)s: see the bound at `pieces`
+constexpr int kRwSplitSlots = 2 * kRwResident;   // pieces of divided items: see the bound at rows_candidate
 constexpr int kRwWarpBatch = 128;             // requests whose division each warp works out itself
 constexpr float kRwSlack = 6.0f;              // log2 by which scores may exceed the running maximum
 
 struct RowsParams {
     PagedAttnParams a;
-    int g_inv;               // ceil(2^16 / G): c / G = c g_inv >> 16 for c < 8
+    int g_inv;               // ceil(2^16 / G): c / G = c g_inv >> 16 for c < 32
     int32_t *counters;       // [kRwSplitSlots], zero between calls
-    float *part;             // [kRwSplitSlots][kRowsMax * D + 2 * kRowsMax]
+    float *part;             // [kRwSplitSlots][kRowsCols * D + 2 * kRowsCols]
     const int32_t *division; // [2][B + 1] from the division kernel where B > kRwWarpBatch, else null
 };
 
@@ -82,6 +86,11 @@ __device__ __forceinline__ RowsTiles rows_tiles(const PagedAttnParams &p, const 
     t.sink_tiles = p.window ? min((sk + kRwTile - 1) / kRwTile, t.first) : 0;
     t.count = t.sink_tiles + max(0, (r.kv + kRwTile - 1) / kRwTile - t.first);
     return t;
+}
+
+// Groups of 8 (row, head) pairs of a request.
+__device__ __forceinline__ int rows_groups(const PagedAttnParams &p, int b) {
+    return (paged_request(p, b).n * p.G + kRowsCols - 1) / kRowsCols;
 }
 
 // Rounds (four tiles) of request b for this kernel: 0 if it has no rows or
@@ -102,10 +111,24 @@ __device__ __forceinline__ int64_t rows_candidate(int64_t s0, int c) {
     return s0 + (c == 0 ? 0 : c == 1 ? (s0 + 3) / 4 : c == 2 ? (s0 + 1) / 2 : s0);
 }
 
-// Where a piece lies.
+// Where a piece lies: its column group comes first, so that those which read the
+// same tokens run side by side.
 struct RowsPiece {
-    int b, split, nsplit, h, slot;   // slot: the first slot of its (request, head) among the divided ones
+    int b, split, nsplit, h, group;
+    int slot;   // the first slot of its item among the divided ones
 };
+
+__device__ __forceinline__ RowsPiece rows_piece(const PagedAttnParams &p, int b, int rest, int nsplit, int slot) {
+    const int groups = rows_groups(p, b), hs = rest / groups;
+    RowsPiece r;
+    r.b = b;
+    r.nsplit = nsplit;
+    r.group = rest - hs * groups;
+    r.h = hs / nsplit;
+    r.split = hs - r.h * nsplit;
+    r.slot = slot + (r.h * groups + r.group) * nsplit;
+    return r;
+}
 
 // ceil(a / x) for 0 <= a < 2^23, 0 < x: `inv` = 1 / x rounded; the estimate is
 // within one of the quotient, and the products are exact.
@@ -118,22 +141,26 @@ __device__ __forceinline__ int ceil_div(int a, int x, float inv) {
 
 // The division by one warp: lane l holds the requests l, l + 32, ...
 struct RowsDivision {
-    int ns[kRwWarpBatch / 32], start[kRwWarpBatch / 32], slot[kRwWarpBatch / 32];   // pieces per head; pieces and
-    int pieces;                                                                      // divided pieces before it
+    int ns[kRwWarpBatch / 32], items[kRwWarpBatch / 32];      // pieces per item, items (heads x column groups)
+    int start[kRwWarpBatch / 32], slot[kRwWarpBatch / 32];    // pieces and divided pieces before it
+    int pieces;
 
     __device__ __forceinline__ void make(const PagedAttnParams &p) {
         constexpr int N = kRwWarpBatch / 32;
         const int lane = threadIdx.x & 31;
-        int r[N], sum = 0;
+        int r[N], sum = 0, all = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            r[i] = lane + 32 * i < p.B ? rows_rounds(p, lane + 32 * i) : 0;   // at most 2^22 each: the sum fits
-            sum += r[i];
+            r[i] = lane + 32 * i < p.B ? rows_rounds(p, lane + 32 * i) : 0;   // at most 2^23 each: the sum fits
+            items[i] = r[i] ? rows_groups(p, lane + 32 * i) : 0;              // of one head for now
+            sum += r[i] * items[i];
+            all += items[i];
         }
-        const int64_t total = (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)sum) * p.Hkv;
+        const int64_t total = (((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)sum >> 16) << 16) +
+                               __reduce_add_sync(0xffffffffu, (uint32_t)sum & 0xffffu)) * p.Hkv;
         const int64_t s0 = max((int64_t)1, (total + kRwResident - 1) / kRwResident);
         int S = (int)min(s0, (int64_t)1 << 22);
-        if (p.B * p.Hkv <= kRwResident) {
+        if ((int)__reduce_add_sync(0xffffffffu, (uint32_t)all) * p.Hkv <= kRwResident) {
             S = (int)rows_candidate(s0, 3);
 #pragma unroll
             for (int c = 2; c >= 0; --c) {
@@ -142,7 +169,7 @@ struct RowsDivision {
                 int n = 0;
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    if (32 * i < p.B) n += ceil_div(r[i], x, inv);
+                    if (32 * i < p.B) n += ceil_div(r[i], x, inv) * items[i];
                 if ((int)__reduce_add_sync(0xffffffffu, (uint32_t)n) * p.Hkv <= kRwResident) S = x;
             }
         }
@@ -153,7 +180,8 @@ struct RowsDivision {
             ns[i] = start[i] = slot[i] = 0;
             if (32 * i >= p.B) continue;
             ns[i] = ceil_div(r[i], S, inv);
-            const int v0 = ns[i] * p.Hkv, v1 = ns[i] > 1 ? v0 : 0;
+            items[i] *= p.Hkv;
+            const int v0 = ns[i] * items[i], v1 = ns[i] > 1 ? v0 : 0;
             int i0 = v0, i1 = v1;
 #pragma unroll
             for (int k = 1; k < 32; k <<= 1) {
@@ -172,17 +200,11 @@ struct RowsDivision {
         int b = -1, rest = 0, n = 1, sl = 0;
 #pragma unroll
         for (int i = 0; i < kRwWarpBatch / 32; ++i)
-            if (piece >= start[i] && piece < start[i] + ns[i] * p.Hkv)
+            if (piece >= start[i] && piece < start[i] + ns[i] * items[i])
                 b = (int)(threadIdx.x & 31) + 32 * i, rest = piece - start[i], n = ns[i], sl = slot[i];
         const int owner = __ffs((int)__ballot_sync(0xffffffffu, b >= 0)) - 1;
-        RowsPiece r;
-        r.b = __shfl_sync(0xffffffffu, b, owner);
-        r.nsplit = __shfl_sync(0xffffffffu, n, owner);
-        rest = __shfl_sync(0xffffffffu, rest, owner);
-        r.h = rest / r.nsplit;
-        r.split = rest - r.h * r.nsplit;
-        r.slot = __shfl_sync(0xffffffffu, sl, owner) + r.h * r.nsplit;
-        return r;
+        return rows_piece(p, __shfl_sync(0xffffffffu, b, owner), __shfl_sync(0xffffffffu, rest, owner),
+                          __shfl_sync(0xffffffffu, n, owner), __shfl_sync(0xffffffffu, sl, owner));
     }
 };
 
@@ -208,17 +230,24 @@ __global__ void __launch_bounds__(kDivThreads) kv4_rows_division_kernel(const __
     __shared__ int red0[32], red1[32];
     int32_t *slot = start + p.B + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t rounds = 0;
-    for (int b = threadIdx.x; b < p.B; b += kDivThreads) rounds += rows_rounds(p, b);
+    int64_t rounds = 0, items = 0;
+    for (int b = threadIdx.x; b < p.B; b += kDivThreads) {
+        const int r = rows_rounds(p, b), g = r ? rows_groups(p, b) : 0;
+        rounds += (int64_t)r * g;
+        items += g;
+    }
     const int64_t total = block_sum(rounds, red) * p.Hkv;
     const int64_t s0 = max((int64_t)1, (total + kRwResident - 1) / kRwResident);
     int64_t S = s0;
-    if ((int64_t)p.B * p.Hkv <= kRwResident) {
+    if (block_sum(items, red) * p.Hkv <= kRwResident) {
         S = rows_candidate(s0, 3);
         for (int c = 2; c >= 0; --c) {
             const int64_t x = rows_candidate(s0, c);
             int64_t n = 0;
-            for (int b = threadIdx.x; b < p.B; b += kDivThreads) n += (rows_rounds(p, b) + x - 1) / x;
+            for (int b = threadIdx.x; b < p.B; b += kDivThreads) {
+                const int r = rows_rounds(p, b);
+                if (r) n += (r + x - 1) / x * rows_groups(p, b);
+            }
             if (block_sum(n, red) * p.Hkv <= kRwResident) S = x;
         }
     }
@@ -226,7 +255,7 @@ __global__ void __launch_bounds__(kDivThreads) kv4_rows_division_kernel(const __
     for (int b0 = 0; b0 < p.B; b0 += kDivThreads) {
         const int b = b0 + threadIdx.x;
         const int ns = b < p.B ? (int)((rows_rounds(p, b) + S - 1) / S) : 0;
-        const int v0 = ns * p.Hkv, v1 = ns > 1 ? v0 : 0;
+        const int v0 = ns ? ns * p.Hkv * rows_groups(p, b) : 0, v1 = ns > 1 ? v0 : 0;
         int i0 = v0, i1 = v1;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -256,14 +285,8 @@ __device__ __forceinline__ RowsPiece find_piece(const PagedAttnParams &p, const 
         if (start[mid] <= piece) lo = mid;
         else hi = mid - 1;
     }
-    RowsPiece r;
-    r.b = lo;
-    const int rest = piece - start[lo];
-    r.nsplit = (start[lo + 1] - start[lo]) / p.Hkv;
-    r.h = rest / r.nsplit;
-    r.split = rest - r.h * r.nsplit;
-    r.slot = start[p.B + 1 + lo] + r.h * r.nsplit;
-    return r;
+    const int items = p.Hkv * rows_groups(p, lo);
+    return rows_piece(p, lo, piece - start[lo], (start[lo + 1] - start[lo]) / items, start[p.B + 1 + lo]);
 }
 
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -300,15 +323,15 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     constexpr int KS = D / 16;        // k-steps of the score product
     constexpr int MT = D / 16;        // m-tiles (16 dims) of the output product
     constexpr int TB = kRwTile * DB;  // bytes of one tensor's tile
-    constexpr int PSZ = kRowsMax * D + 2 * kRowsMax;
+    constexpr int PSZ = kRowsCols * D + 2 * kRowsCols;
     constexpr float kNone = -1e30f;   // below every score: a running maximum that has seen nothing
     constexpr int CPT = DB / 16;      // 16-byte chunks per vector
     constexpr int CPL = TB / 16 / 32; // chunks a lane copies per tile
-    static_assert(kRowsMax * D * 4 <= 3 * TB, "the merge slots fit the code buffers");
+    static_assert(kRowsCols * D * 4 <= 3 * TB, "the merge slots fit the code buffers");
     const PagedAttnParams &p = w.a;
     extern __shared__ __align__(128) uint8_t rw_smem[];
-    __shared__ float mw[kRwWarps][kRowsMax], lw[kRwWarps][kRowsMax];
-    __shared__ float mc[kRowsMax], lc[kRowsMax];
+    __shared__ float mw[kRwWarps][kRowsCols], lw[kRwWarps][kRowsCols];
+    __shared__ float mc[kRowsCols], lc[kRowsCols];
     __shared__ __align__(16) float2 kf_s[kRwWarps][kRwTile];   // per token: 2^24 s c, -z s c (c = log2(e) / sqrt(D))
     __shared__ float vf_s[kRwWarps][kRwTile];                  // value scale * 2^(8 - E)
     __shared__ __align__(16) __half vz_s[kRwWarps][kRwTile];   // value zero
@@ -353,7 +376,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         const int each = rounds / nsplit, extra = rounds - each * nsplit;   // the first `extra` pieces take one more
         const int k_begin = (split * each + min(split, extra)) * kRwWarps;
         const int k_end = min(k_begin + (each + (split < extra ? 1 : 0)) * kRwWarps, tl.count);
-        const int cols = r.n * p.G;
+        const int col0 = pc.group * kRowsCols, cols = min(r.n * p.G - col0, kRowsCols);   // the piece's columns
         const int pos0 = r.kv - r.n;   // position of the first row
 
         auto tile_t0 = [&](int k) {
@@ -441,9 +464,9 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         uint32_t qf[KS][2];
         float sq2[2];
         {
-            const int i0 = (gid * w.g_inv) >> 16;   // gid / G
+            const int col = col0 + gid, i0 = (col * w.g_inv) >> 16;   // i0 = col / G
             const __half *qrow = p.q + (int64_t)(r.row0 + i0) * p.q_stride +
-                                 (int64_t)(h * p.G + gid - i0 * p.G) * D + tig * (D / 4);
+                                 (int64_t)(h * p.G + col - i0 * p.G) * D + tig * (D / 4);
             const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
             float sq = 0.0f;
 #pragma unroll
@@ -471,7 +494,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         // Positions of the lane's two columns; columns >= cols see every token.
         int cpos[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) cpos[c] = 2 * tig + c < cols ? pos0 + (((2 * tig + c) * w.g_inv) >> 16) : r.kv - 1;
+        for (int c = 0; c < 2; ++c) cpos[c] = 2 * tig + c < cols ? pos0 + (((col0 + 2 * tig + c) * w.g_inv) >> 16) : r.kv - 1;
 
         float m2[2] = {kNone, kNone};    // running maximum of columns 2 tig, 2 tig + 1
         float l2[2] = {0.0f, 0.0f};      // running sum of the same columns
@@ -692,8 +715,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             lw[warp][2 * tig + 1] = l2[1];
         }
         __syncthreads();
-        float *ow = reinterpret_cast<float *>(rw_smem);   // [kRwWarps][kRowsMax][D]
-        if (tid < kRowsMax) {
+        float *ow = reinterpret_cast<float *>(rw_smem);   // [kRwWarps][kRowsCols][D]
+        if (tid < kRowsCols) {
             float M = kNone;
             for (int x = 0; x < kRwWarps; ++x) M = fmaxf(M, mw[x][tid]);
             float L = 0.0f;
@@ -708,7 +731,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             const int g = 2 * tig + c;
             if (g < cols) {
                 const float f = exp2f(m2[c] - mc[g]) * unit;
-                float *dst = ow + (warp * kRowsMax + g) * D;
+                float *dst = ow + (warp * kRowsCols + g) * D;
 #pragma unroll
                 for (int u = 0; u < UB; ++u)
                     *reinterpret_cast<float4 *>(dst + 4 * (8 * u + gid)) =
@@ -719,13 +742,13 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         }
         __syncthreads();
         auto out_at = [&](int i) {   // element i of [columns][D]
-            const int c = i / D, i0 = (c * w.g_inv) >> 16;   // i0 = c / G
+            const int c = col0 + i / D, i0 = (c * w.g_inv) >> 16;   // i0 = c / G
             return p.out + (int64_t)(r.row0 + i0) * p.out_stride + (int64_t)(h * p.G + c - i0 * p.G) * D + (i % D);
         };
         if (nsplit == 1) {
             for (int i = tid; i < cols * D; i += kRwThreads) {
                 float sum = ow[i];
-                for (int x = 1; x < kRwWarps; ++x) sum += ow[x * kRowsMax * D + i];
+                for (int x = 1; x < kRwWarps; ++x) sum += ow[x * kRowsCols * D + i];
                 const float L = lc[i / D];
                 *out_at(i) = __float2half_rn(L > 0.0f ? sum / L : 0.0f);
             }
@@ -737,25 +760,25 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             float *part = w.part + (int64_t)(s0 + split) * PSZ;
             for (int i = tid; i < cols * D; i += kRwThreads) {
                 float sum = ow[i];
-                for (int x = 1; x < kRwWarps; ++x) sum += ow[x * kRowsMax * D + i];
+                for (int x = 1; x < kRwWarps; ++x) sum += ow[x * kRowsCols * D + i];
                 part[i] = sum;
             }
-            if (tid < kRowsMax) {
-                part[kRowsMax * D + tid] = mc[tid];
-                part[kRowsMax * D + kRowsMax + tid] = lc[tid];
+            if (tid < kRowsCols) {
+                part[kRowsCols * D + tid] = mc[tid];
+                part[kRowsCols * D + kRowsCols + tid] = lc[tid];
             }
             __syncthreads();   // every store of the CTA precedes the arrival (cumulative release)
             if (tid == 0) last_s = atom_add_acq_rel_gpu(w.counters + s0, 1) == nsplit - 1;
             __syncthreads();
             if (last_s) {
                 const float *base = w.part + (int64_t)s0 * PSZ;
-                if (tid < kRowsMax) {
+                if (tid < kRowsCols) {
                     float M = kNone;
-                    for (int c = 0; c < nsplit; ++c) M = fmaxf(M, __ldcg(base + c * PSZ + kRowsMax * D + tid));
+                    for (int c = 0; c < nsplit; ++c) M = fmaxf(M, __ldcg(base + c * PSZ + kRowsCols * D + tid));
                     float L = 0.0f;
                     for (int c = 0; c < nsplit; ++c)
-                        L += exp2f(__ldcg(base + c * PSZ + kRowsMax * D + tid) - M) *
-                             __ldcg(base + c * PSZ + kRowsMax * D + kRowsMax + tid);
+                        L += exp2f(__ldcg(base + c * PSZ + kRowsCols * D + tid) - M) *
+                             __ldcg(base + c * PSZ + kRowsCols * D + kRowsCols + tid);
                     mc[tid] = M;
                     lc[tid] = L;
                 }
@@ -764,7 +787,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                     const int g = i / D;
                     float O = 0.0f;
                     for (int c = 0; c < nsplit; ++c)
-                        O += exp2f(__ldcg(base + c * PSZ + kRowsMax * D + g) - mc[g]) * __ldcg(base + c * PSZ + i);
+                        O += exp2f(__ldcg(base + c * PSZ + kRowsCols * D + g) - mc[g]) * __ldcg(base + c * PSZ + i);
                     *out_at(i) = __float2half_rn(lc[g] > 0.0f ? O / lc[g] : 0.0f);
                 }
                 if (tid == 0) w.counters[s0] = 0;   // nobody arrives on it again in this call
@@ -800,7 +823,7 @@ cudaError_t launch(const RowsParams &w, cudaStream_t stream) {
 // Workspace: counters, partial results, the division of large batches.
 size_t rows_workspace_bytes(int64_t B, int64_t D) {
     return (size_t)align256(4 * kRwSplitSlots) +
-           (size_t)align256(4 * (int64_t)kRwSplitSlots * (kRowsMax * D + 2 * kRowsMax)) +
+           (size_t)align256(4 * (int64_t)kRwSplitSlots * (kRowsCols * D + 2 * kRowsCols)) +
            (B > kRwWarpBatch ? (size_t)align256(8 * (B + 1)) : 0);
 }
 
@@ -812,7 +835,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cud
     w.counters = reinterpret_cast<int32_t *>(at);
     at += align256(4 * kRwSplitSlots);
     w.part = reinterpret_cast<float *>(at);
-    at += align256(4 * (int64_t)kRwSplitSlots * (kRowsMax * D + 2 * kRowsMax));
+    at += align256(4 * (int64_t)kRwSplitSlots * (kRowsCols * D + 2 * kRowsCols));
     w.division = nullptr;
     if (p.B > kRwWarpBatch) {
         w.division = reinterpret_cast<int32_t *>(at);
