@@ -61,16 +61,16 @@ constexpr int kRwWarps = 4;
 constexpr int kRwThreads = 32 * kRwWarps;
 constexpr int kRwTile = 64;                   // tokens per warp tile
 constexpr int kRwResident = 4 * 148;          // CTAs that run at once
-constexpr int kRwSplitSlots = 2 * kRwResident;   // pieces of divided items: see the bound at rows_candidate
+constexpr int kRwStart = 2;                   // rounds that fit in the time in which an item starts and is merged
 constexpr int kRwWarpBatch = 128;             // requests whose division each warp works out itself
 constexpr float kRwSlack = 6.0f;              // log2 by which scores may exceed the running maximum
 
 struct RowsParams {
     PagedAttnParams a;
     int g_inv;               // ceil(2^16 / G): c / G = c g_inv >> 16 for c < 32
-    int32_t *counters;       // [kRwSplitSlots], zero between calls
-    float *part;             // [kRwSplitSlots][kRowsCols * D + 2 * kRowsCols]
-    const int32_t *division; // [2][B + 1] from the division kernel where B > kRwWarpBatch, else null
+    int32_t *counters;       // [kRwResident], zero between calls
+    float *part;             // [2 kRwResident][kRowsCols * D + 2 * kRowsCols]
+    const int64_t *first;    // [B + 2] from the division kernel where B > kRwWarpBatch, else null
 };
 
 // A request's tiles: [0, sink_tiles) and [first, end) in units of 64 tokens.
@@ -93,6 +93,8 @@ __device__ __forceinline__ int rows_groups(const PagedAttnParams &p, int b) {
     return (paged_request(p, b).n * p.G + kRowsCols - 1) / kRowsCols;
 }
 
+__device__ __forceinline__ int rows_items(const PagedAttnParams &p, int b) { return p.Hkv * rows_groups(p, b); }
+
 // Rounds (four tiles) of request b for this kernel: 0 if it has no rows or
 // too many; one where it has rows but no token (zeros are written).
 __device__ __forceinline__ int rows_rounds(const PagedAttnParams &p, int b) {
@@ -101,192 +103,182 @@ __device__ __forceinline__ int rows_rounds(const PagedAttnParams &p, int b) {
     return max(1, (rows_tiles(p, r).count + kRwWarps - 1) / kRwWarps);
 }
 
-// Rounds per piece, from the batch's rounds (all heads) and the sums over the
-// batch of ceil(rounds / S) for the candidates S.
-//
-// S >= total / C (C resident CTAs) bounds the divided pieces: a request is
-// divided when x = rounds / S > 1, into ceil(x) <= 2 x pieces per head, so
-// there are at most 2 total / S <= 2 C of them.
-__device__ __forceinline__ int64_t rows_candidate(int64_t s0, int c) {
-    return s0 + (c == 0 ? 0 : c == 1 ? (s0 + 3) / 4 : c == 2 ? (s0 + 1) / 2 : s0);
-}
-
-// Where a piece lies: its column group comes first, so that those which read the
-// same tokens run side by side.
-struct RowsPiece {
-    int b, split, nsplit, h, group;
-    int slot;   // the first slot of its item among the divided ones
+// The division. A (request, KV head, column group) is an item of so many
+// rounds, and of kRwStart rounds' time before the first. The items follow one
+// another by request, head, group; CTA c takes [c S, (c + 1) S) of that
+// sequence, S = ceil(total / resident CTAs): as much for each whatever the
+// lengths. Its first segment may be the end or a part of an item, its last a
+// beginning; those between are whole. Where one item per CTA ends about as
+// soon (the longest is hardly above S, and a second segment costs a start),
+// every item counts as long as the longest and none is divided.
+struct RowsWork {
+    int S;            // rounds per CTA
+    int same;         // the length that every item counts as, or 0: its own
+    int remaining, done;   // rounds of this CTA, and those of them that are done
+    int b, item, offset;   // where the next begins: item of request b, round of the item
 };
 
-__device__ __forceinline__ RowsPiece rows_piece(const PagedAttnParams &p, int b, int rest, int nsplit, int slot) {
-    const int groups = rows_groups(p, b), hs = rest / groups;
-    RowsPiece r;
-    r.b = b;
-    r.nsplit = nsplit;
-    r.group = rest - hs * groups;
-    r.h = hs / nsplit;
-    r.split = hs - r.h * nsplit;
-    r.slot = slot + (r.h * groups + r.group) * nsplit;
-    return r;
+// What the end of a segment needs of it.
+struct RowsSegment {
+    int count;             // rounds, the start's included
+    int before, nsplit;    // CTAs before this one and CTAs that the item's rounds are divided over
+    int row0, h, col0, cols;
+    bool last_item;        // of its request
+};
+
+// Length of request b's items: 0 without rows for this kernel.
+__device__ __forceinline__ int rows_length(const PagedAttnParams &p, int b, int same) {
+    const int rounds = rows_rounds(p, b);
+    return rounds == 0 ? 0 : same ? same : rounds + kRwStart;
 }
 
-// ceil(a / x) for 0 <= a < 2^23, 0 < x: `inv` = 1 / x rounded; the estimate is
-// within one of the quotient, and the products are exact.
-__device__ __forceinline__ int ceil_div(int a, int x, float inv) {
+// From the batch's items, the sum of their lengths and the longest: S, same
+// and the sum that results.
+__device__ __forceinline__ int64_t rows_shares(RowsWork &w, int64_t items, int64_t total, int longest) {
+    w.S = total <= kRwResident ? 1 : (int)((uint64_t)(total + kRwResident - 1) / kRwResident);
+    w.same = 0;
+    if (items <= kRwResident && longest <= w.S + kRwStart) {
+        w.S = w.same = longest;
+        return items * longest;
+    }
+    return total;
+}
+
+// Where x of the sequence lies, in_request behind the first of request b's.
+__device__ __forceinline__ void rows_begin(const PagedAttnParams &p, RowsWork &w, int64_t total, int64_t x, int b,
+                                           int64_t in_request) {
+    const int length = rows_length(p, b, w.same);
+    w.remaining = (int)min((int64_t)w.S, total - x);
+    w.done = 0;
+    w.b = b;
+    w.item = (int)((uint64_t)in_request / (uint32_t)length);
+    w.offset = (int)(in_request - (int64_t)w.item * length);
+}
+
+// floor(a / x) for 0 <= a < 2^24, 0 < x < 2^27: `inv` = 1 / x rounded; the
+// estimate is within one of the quotient, and the products fit.
+__device__ __forceinline__ int floor_div(int a, int x, float inv) {
     int q = (int)((float)a * inv);
-    q -= q * x >= a + x ? 1 : 0;
-    q += q * x < a ? 1 : 0;
-    return q + (q * x < a ? 1 : 0);
+    q -= q * x > a ? 1 : 0;
+    return q + ((q + 1) * x <= a ? 1 : 0);
 }
 
-// The division by one warp: lane l holds the requests l, l + 32, ...
-struct RowsDivision {
-    int ns[kRwWarpBatch / 32], items[kRwWarpBatch / 32];      // pieces per item, items (heads x column groups)
-    int start[kRwWarpBatch / 32], slot[kRwWarpBatch / 32];    // pieces and divided pieces before it
-    int pieces;
-
-    __device__ __forceinline__ void make(const PagedAttnParams &p) {
-        constexpr int N = kRwWarpBatch / 32;
-        const int lane = threadIdx.x & 31;
-        int r[N], sum = 0, all = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            r[i] = lane + 32 * i < p.B ? rows_rounds(p, lane + 32 * i) : 0;   // at most 2^23 each: the sum fits
-            items[i] = r[i] ? rows_groups(p, lane + 32 * i) : 0;              // of one head for now
-            sum += r[i] * items[i];
-            all += items[i];
-        }
-        const int64_t total = (((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)sum >> 16) << 16) +
-                               __reduce_add_sync(0xffffffffu, (uint32_t)sum & 0xffffu)) * p.Hkv;
-        const int64_t s0 = max((int64_t)1, (total + kRwResident - 1) / kRwResident);
-        int S = (int)min(s0, (int64_t)1 << 22);
-        if ((int)__reduce_add_sync(0xffffffffu, (uint32_t)all) * p.Hkv <= kRwResident) {
-            S = (int)rows_candidate(s0, 3);
-#pragma unroll
-            for (int c = 2; c >= 0; --c) {
-                const int x = (int)rows_candidate(s0, c);
-                const float inv = __frcp_rn((float)x);
-                int n = 0;
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (32 * i < p.B) n += ceil_div(r[i], x, inv) * items[i];
-                if ((int)__reduce_add_sync(0xffffffffu, (uint32_t)n) * p.Hkv <= kRwResident) S = x;
-            }
-        }
-        const float inv = __frcp_rn((float)S);
-        int base0 = 0, base1 = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            ns[i] = start[i] = slot[i] = 0;
-            if (32 * i >= p.B) continue;
-            ns[i] = ceil_div(r[i], S, inv);
-            items[i] *= p.Hkv;
-            const int v0 = ns[i] * items[i], v1 = ns[i] > 1 ? v0 : 0;
-            int i0 = v0, i1 = v1;
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const int u0 = __shfl_up_sync(0xffffffffu, i0, k), u1 = __shfl_up_sync(0xffffffffu, i1, k);
-                if (lane >= k) i0 += u0, i1 += u1;
-            }
-            start[i] = base0 + i0 - v0;
-            slot[i] = base1 + i1 - v1;
-            base0 += __shfl_sync(0xffffffffu, i0, 31);
-            base1 += __shfl_sync(0xffffffffu, i1, 31);
-        }
-        pieces = base0;
+// A batch of up to kRwWarpBatch requests, by each warp: lane l holds the
+// requests l per, l per + 1, ... false: nothing is left for this CTA.
+__device__ __forceinline__ bool rows_divide(const PagedAttnParams &p, RowsWork &w) {
+    const int lane = threadIdx.x & 31, per = (p.B + 31) >> 5;
+    int64_t sum = 0;
+    int items = 0, longest = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = lane * per + i, n = b < p.B ? rows_length(p, b, 0) : 0;
+        if (n == 0) continue;
+        const int k = rows_items(p, b);
+        sum += (int64_t)n * k;
+        items += k;
+        longest = max(longest, n);
     }
-
-    __device__ __forceinline__ RowsPiece find(const PagedAttnParams &p, int piece) const {
-        int b = -1, rest = 0, n = 1, sl = 0;
+    int64_t upto = sum;
 #pragma unroll
-        for (int i = 0; i < kRwWarpBatch / 32; ++i)
-            if (piece >= start[i] && piece < start[i] + ns[i] * items[i])
-                b = (int)(threadIdx.x & 31) + 32 * i, rest = piece - start[i], n = ns[i], sl = slot[i];
-        const int owner = __ffs((int)__ballot_sync(0xffffffffu, b >= 0)) - 1;
-        return rows_piece(p, __shfl_sync(0xffffffffu, b, owner), __shfl_sync(0xffffffffu, rest, owner),
-                          __shfl_sync(0xffffffffu, n, owner), __shfl_sync(0xffffffffu, sl, owner));
+    for (int k = 1; k < 32; k <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, upto, k);
+        if (lane >= k) upto += u;
     }
-};
-
-// The same division of a large batch, by one CTA into start[B + 1] (first
-// piece of each request) and slot[B + 1] (first slot of each divided one).
-constexpr int kDivThreads = 1024;
-
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *red) {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = red[threadIdx.x & 31];
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
-    return t;
-}
-
-__global__ void __launch_bounds__(kDivThreads) kv4_rows_division_kernel(const __grid_constant__ PagedAttnParams p,
-                                                                        int32_t *start) {
-    __shared__ int64_t red[32];
-    __shared__ int red0[32], red1[32];
-    int32_t *slot = start + p.B + 1;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t rounds = 0, items = 0;
-    for (int b = threadIdx.x; b < p.B; b += kDivThreads) {
-        const int r = rows_rounds(p, b), g = r ? rows_groups(p, b) : 0;
-        rounds += (int64_t)r * g;
-        items += g;
-    }
-    const int64_t total = block_sum(rounds, red) * p.Hkv;
-    const int64_t s0 = max((int64_t)1, (total + kRwResident - 1) / kRwResident);
-    int64_t S = s0;
-    if (block_sum(items, red) * p.Hkv <= kRwResident) {
-        S = rows_candidate(s0, 3);
-        for (int c = 2; c >= 0; --c) {
-            const int64_t x = rows_candidate(s0, c);
-            int64_t n = 0;
-            for (int b = threadIdx.x; b < p.B; b += kDivThreads) {
-                const int r = rows_rounds(p, b);
-                if (r) n += (r + x - 1) / x * rows_groups(p, b);
-            }
-            if (block_sum(n, red) * p.Hkv <= kRwResident) S = x;
-        }
-    }
-    int base0 = 0, base1 = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kDivThreads) {
-        const int b = b0 + threadIdx.x;
-        const int ns = b < p.B ? (int)((rows_rounds(p, b) + S - 1) / S) : 0;
-        const int v0 = ns ? ns * p.Hkv * rows_groups(p, b) : 0, v1 = ns > 1 ? v0 : 0;
-        int i0 = v0, i1 = v1;
+    const int64_t total = rows_shares(w, __reduce_add_sync(0xffffffffu, (uint32_t)items),
+                                      __shfl_sync(0xffffffffu, upto, 31),
+                                      (int)__reduce_max_sync(0xffffffffu, (uint32_t)longest));
+    const int64_t x = (int64_t)blockIdx.x * w.S;
+    if (x >= total) return false;
+    if (w.same) {
+        upto = (int64_t)items * w.same;
+        sum = upto;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
-            const int u0 = __shfl_up_sync(0xffffffffu, i0, k), u1 = __shfl_up_sync(0xffffffffu, i1, k);
-            if (lane >= k) i0 += u0, i1 += u1;
-        }
-        __syncthreads();
-        if (lane == 31) red0[warp] = i0, red1[warp] = i1;
-        __syncthreads();
-        int o0 = base0, o1 = base1;
-        for (int x = 0; x < kDivThreads / 32; ++x) {
-            if (x < warp) o0 += red0[x], o1 += red1[x];
-            base0 += red0[x], base1 += red1[x];
-        }
-        if (b < p.B) {
-            start[b] = o0 + i0 - v0;
-            slot[b] = o1 + i1 - v1;
+            const int64_t u = __shfl_up_sync(0xffffffffu, upto, k);
+            if (lane >= k) upto += u;
         }
     }
-    if (threadIdx.x == 0) start[p.B] = base0, slot[p.B] = base1;
+    const int owner = __ffs((int)__ballot_sync(0xffffffffu, upto > x)) - 1;
+    int64_t rest = x - __shfl_sync(0xffffffffu, upto - sum, owner);
+    int b = owner * per;
+    for (;; ++b) {
+        const int64_t n = (int64_t)rows_length(p, b, w.same) * rows_items(p, b);
+        if (rest < n) break;
+        rest -= n;
+    }
+    rows_begin(p, w, total, x, b, rest);
+    return true;
 }
 
-__device__ __forceinline__ RowsPiece find_piece(const PagedAttnParams &p, const int32_t *start, int piece) {
-    int lo = 0, hi = p.B - 1;   // the last request that starts at or before the piece
+// The same of a large batch, by one CTA: what precedes each request, the sum,
+// and `S`, `same`.
+constexpr int kDivThreads = 1024;
+
+__global__ void __launch_bounds__(kDivThreads) kv4_rows_division_kernel(const __grid_constant__ PagedAttnParams p,
+                                                                        int64_t *first) {
+    __shared__ int64_t red[32], red_items[32];
+    __shared__ int red_longest[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t total = 0, items = 0;
+    int longest = 0;
+    for (int b = threadIdx.x; b < p.B; b += kDivThreads) {
+        const int n = rows_length(p, b, 0), k = n ? rows_items(p, b) : 0;
+        total += (int64_t)n * k;
+        items += k;
+        longest = max(longest, n);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, k);
+        items += __shfl_xor_sync(0xffffffffu, items, k);
+    }
+    longest = (int)__reduce_max_sync(0xffffffffu, (uint32_t)longest);
+    if (lane == 0) red[warp] = total, red_items[warp] = items, red_longest[warp] = longest;
+    __syncthreads();
+    total = 0, items = 0, longest = 0;
+    for (int x = 0; x < kDivThreads / 32; ++x) {
+        total += red[x], items += red_items[x];
+        longest = max(longest, red_longest[x]);
+    }
+    RowsWork w;
+    total = rows_shares(w, items, total, longest);
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kDivThreads) {
+        const int b = b0 + threadIdx.x;
+        const int n = b < p.B ? rows_length(p, b, w.same) : 0;
+        const int64_t v = n ? (int64_t)n * rows_items(p, b) : 0;
+        int64_t upto = v;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, upto, k);
+            if (lane >= k) upto += u;
+        }
+        __syncthreads();
+        if (lane == 31) red[warp] = upto;
+        __syncthreads();
+        int64_t before = base;
+        for (int x = 0; x < kDivThreads / 32; ++x) {
+            if (x < warp) before += red[x];
+            base += red[x];
+        }
+        if (b < p.B) first[b] = before + upto - v;
+    }
+    if (threadIdx.x == 0) first[p.B] = total, first[p.B + 1] = (int64_t)w.S << 32 | (uint32_t)w.same;
+}
+
+__device__ __forceinline__ bool rows_find(const PagedAttnParams &p, RowsWork &w, const int64_t *first) {
+    const int64_t total = first[p.B], shares = first[p.B + 1];
+    w.S = (int)(shares >> 32);
+    w.same = (int)(uint32_t)shares;
+    const int64_t x = (int64_t)blockIdx.x * w.S;
+    if (x >= total) return false;
+    int lo = 0, hi = p.B - 1;   // the last request that begins at or before x: it has rounds
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= piece) lo = mid;
+        if (first[mid] <= x) lo = mid;
         else hi = mid - 1;
     }
-    const int items = p.Hkv * rows_groups(p, lo);
-    return rows_piece(p, lo, piece - start[lo], (start[lo + 1] - start[lo]) / items, start[p.B + 1 + lo]);
+    rows_begin(p, w, total, x, lo, x - first[lo]);
+    return true;
 }
 
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -328,6 +320,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     constexpr int CPT = DB / 16;      // 16-byte chunks per vector
     constexpr int CPL = TB / 16 / 32; // chunks a lane copies per tile
     static_assert(kRowsCols * D * 4 <= 3 * TB, "the merge slots fit the code buffers");
+    static_assert(kRwResident * kRowsCols * 4 <= kRwWarps * (3 * TB + kRwTile * 16), "and the segments' factors");
     const PagedAttnParams &p = w.a;
     extern __shared__ __align__(128) uint8_t rw_smem[];
     __shared__ float mw[kRwWarps][kRowsCols], lw[kRwWarps][kRowsCols];
@@ -336,6 +329,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     __shared__ float vf_s[kRwWarps][kRwTile];                  // value scale * 2^(8 - E)
     __shared__ __align__(16) __half vz_s[kRwWarps][kRwTile];   // value zero
     __shared__ int last_s;
+    __shared__ RowsWork work_s;       // kept here and not in registers while the tiles are walked
+    __shared__ RowsSegment seg_s;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -357,26 +352,39 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     const int64_t v_minus_k = p.v_codes - p.k_codes;              // bytes
     const int64_t vp_minus_kp = reinterpret_cast<const uint8_t *>(p.v_params) - reinterpret_cast<const uint8_t *>(p.k_params);
 
-    for (int piece = blockIdx.x, pieces;; piece += gridDim.x) {
-        RowsPiece pc;
-        if (w.division == nullptr) {
-            RowsDivision dv;   // again for every piece: few CTAs take two, and it costs no registers meanwhile
-            dv.make(p);
-            pieces = dv.pieces;
-            if (piece < pieces) pc = dv.find(p, piece);
-        } else {
-            pieces = w.division[p.B];
-            if (piece < pieces) pc = find_piece(p, w.division, piece);
-        }
-        if (piece >= pieces) return;
-        const int b = pc.b, h = pc.h, split = pc.split, nsplit = pc.nsplit;
+    {
+        RowsWork wk;
+        if (!(w.first == nullptr ? rows_divide(p, wk) : rows_find(p, wk, w.first))) return;
+        if (tid == 0) work_s = wk;
+    }
+    for (;;) {
+        __syncthreads();   // work_s is written, and the last segment's merge done with the buffers
+        const int b = work_s.b;
         const PagedRequest r = paged_request(p, b);
         const RowsTiles tl = rows_tiles(p, r);
         const int rounds = max(1, (tl.count + kRwWarps - 1) / kRwWarps);
-        const int each = rounds / nsplit, extra = rounds - each * nsplit;   // the first `extra` pieces take one more
-        const int k_begin = (split * each + min(split, extra)) * kRwWarps;
-        const int k_end = min(k_begin + (each + (split < extra ? 1 : 0)) * kRwWarps, tl.count);
-        const int col0 = pc.group * kRowsCols, cols = min(r.n * p.G - col0, kRowsCols);   // the piece's columns
+        const int groups = (r.n * p.G + kRowsCols - 1) / kRowsCols;
+        const int h = work_s.item / groups, group = work_s.item - h * groups;
+        const int length = work_s.same ? work_s.same : rounds + kRwStart;
+        const int count = min(length - work_s.offset, work_s.remaining - work_s.done);   // of this segment
+        const int round0 = max(work_s.offset - kRwStart, 0), round1 = min(work_s.offset + count - kRwStart, rounds);
+        const int k_begin = round0 * kRwWarps, k_end = min(round1 * kRwWarps, tl.count);
+        const int col0 = group * kRowsCols, cols = min(r.n * p.G - col0, kRowsCols);   // the item's columns
+        if (tid == 0) {
+            // The item's rounds lie with the CTAs blockIdx.x - before ... of
+            // which there are nsplit: `ahead` of its rounds precede this CTA's first.
+            const int S = work_s.S;
+            const float inv = __frcp_rn((float)S);
+            const int ahead = round0 ? round0 : -(work_s.done + kRwStart - work_s.offset);
+            seg_s.before = ahead > 0 ? floor_div(ahead + S - 1, S, inv) : 0;
+            seg_s.nsplit = round0 < round1 ? seg_s.before + floor_div(rounds - 1 - ahead, S, inv) + 1 : 0;
+            seg_s.row0 = r.row0;
+            seg_s.h = h;
+            seg_s.col0 = col0;
+            seg_s.cols = cols;
+            seg_s.count = count;
+            seg_s.last_item = work_s.item + 1 == p.Hkv * groups;
+        }
         const int pos0 = r.kv - r.n;   // position of the first row
 
         auto tile_t0 = [&](int k) {
@@ -714,7 +722,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             lw[warp][2 * tig] = l2[0];
             lw[warp][2 * tig + 1] = l2[1];
         }
-        __syncthreads();
+        __syncthreads();   // (and seg_s is written)
+        const RowsSegment seg = seg_s;
         float *ow = reinterpret_cast<float *>(rw_smem);   // [kRwWarps][kRowsCols][D]
         if (tid < kRowsCols) {
             float M = kNone;
@@ -729,7 +738,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int g = 2 * tig + c;
-            if (g < cols) {
+            if (g < seg.cols) {
                 const float f = exp2f(m2[c] - mc[g]) * unit;
                 float *dst = ow + (warp * kRowsCols + g) * D;
 #pragma unroll
@@ -741,60 +750,104 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             }
         }
         __syncthreads();
-        auto out_at = [&](int i) {   // element i of [columns][D]
-            const int c = col0 + i / D, i0 = (c * w.g_inv) >> 16;   // i0 = c / G
-            return p.out + (int64_t)(r.row0 + i0) * p.out_stride + (int64_t)(h * p.G + c - i0 * p.G) * D + (i % D);
+        // Four neighbouring dims per thread, the warps in order.
+        auto warps_sum = [&](int i) {
+            float4 sum = *reinterpret_cast<const float4 *>(ow + 4 * i);
+#pragma unroll
+            for (int x = 1; x < kRwWarps; ++x) {
+                const float4 v = *reinterpret_cast<const float4 *>(ow + x * kRowsCols * D + 4 * i);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+            return sum;
         };
-        if (nsplit == 1) {
-            for (int i = tid; i < cols * D; i += kRwThreads) {
-                float sum = ow[i];
-                for (int x = 1; x < kRwWarps; ++x) sum += ow[x * kRowsCols * D + i];
-                const float L = lc[i / D];
-                *out_at(i) = __float2half_rn(L > 0.0f ? sum / L : 0.0f);
-            }
+        auto store_out = [&](int i, const float4 &v, float L) {
+            const int c = seg.col0 + 4 * i / D, i0 = (c * w.g_inv) >> 16;   // i0 = c / G
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                h2[e] = half2_bits(L > 0.0f ? __floats2half2_rn(x[2 * e] / L, x[2 * e + 1] / L) : __floats2half2_rn(0.0f, 0.0f));
+            *reinterpret_cast<uint2 *>(p.out + (int64_t)(seg.row0 + i0) * p.out_stride +
+                                       (int64_t)(seg.h * p.G + c - i0 * p.G) * D + 4 * i % D) = make_uint2(h2[0], h2[1]);
+        };
+        if (seg.nsplit == 0) {   // the start of an item whose rounds lie behind this CTA's
+        } else if (seg.nsplit == 1) {
+            for (int i = tid; i < seg.cols * (D / 4); i += kRwThreads) store_out(i, warps_sum(i), lc[4 * i / D]);
         } else {
-            // Several pieces of this (request, head): store this one's
-            // unnormalised sums with its maxima and weights, arrive, and let
-            // the last arriver combine.
-            const int s0 = pc.slot;
-            float *part = w.part + (int64_t)(s0 + split) * PSZ;
-            for (int i = tid; i < cols * D; i += kRwThreads) {
-                float sum = ow[i];
-                for (int x = 1; x < kRwWarps; ++x) sum += ow[x * kRowsCols * D + i];
-                part[i] = sum;
-            }
+            // Store this segment's unnormalised sums with its maxima and
+            // weights, arrive, and let the last arriver combine. A CTA has
+            // two slots: for an item that began before it, and for one that ends behind it.
+            const int c0 = (int)blockIdx.x - seg.before;
+            float *part = w.part + (int64_t)(2 * blockIdx.x + (seg.before ? 0 : 1)) * PSZ;
+            for (int i = tid; i < seg.cols * (D / 4); i += kRwThreads) reinterpret_cast<float4 *>(part)[i] = warps_sum(i);
             if (tid < kRowsCols) {
                 part[kRowsCols * D + tid] = mc[tid];
                 part[kRowsCols * D + kRowsCols + tid] = lc[tid];
             }
             __syncthreads();   // every store of the CTA precedes the arrival (cumulative release)
-            if (tid == 0) last_s = atom_add_acq_rel_gpu(w.counters + s0, 1) == nsplit - 1;
+            if (tid == 0) last_s = atom_add_acq_rel_gpu(w.counters + c0, 1) == seg.nsplit - 1;
             __syncthreads();
             if (last_s) {
-                const float *base = w.part + (int64_t)s0 * PSZ;
-                if (tid < kRowsCols) {
-                    float M = kNone;
-                    for (int c = 0; c < nsplit; ++c) M = fmaxf(M, __ldcg(base + c * PSZ + kRowsCols * D + tid));
-                    float L = 0.0f;
-                    for (int c = 0; c < nsplit; ++c)
-                        L += exp2f(__ldcg(base + c * PSZ + kRowsCols * D + tid) - M) *
-                             __ldcg(base + c * PSZ + kRowsCols * D + kRowsCols + tid);
-                    mc[tid] = M;
-                    lc[tid] = L;
+                auto base = [&](int c) { return w.part + (int64_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * PSZ; };
+                // Each segment's factor per column, 2^(its maximum - the
+                // greatest), over the idle buffers.
+                float *fs = reinterpret_cast<float *>(rw_smem);   // [seg.nsplit][kRowsCols]
+                constexpr int per = kRwThreads / kRowsCols;
+                const int g = tid % kRowsCols;
+                float M = kNone;
+#pragma unroll 4
+                for (int c = tid / kRowsCols; c < seg.nsplit; c += per) {
+                    const float m = __ldcg(base(c) + kRowsCols * D + g);
+                    fs[c * kRowsCols + g] = m;
+                    M = fmaxf(M, m);
                 }
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+                if (lane < kRowsCols) mw[warp][lane] = M;
                 __syncthreads();
-                for (int i = tid; i < cols * D; i += kRwThreads) {
-                    const int g = i / D;
-                    float O = 0.0f;
-                    for (int c = 0; c < nsplit; ++c)
-                        O += exp2f(__ldcg(base + c * PSZ + kRowsCols * D + g) - mc[g]) * __ldcg(base + c * PSZ + i);
-                    *out_at(i) = __float2half_rn(lc[g] > 0.0f ? O / lc[g] : 0.0f);
+                M = fmaxf(fmaxf(mw[0][g], mw[1][g]), fmaxf(mw[2][g], mw[3][g]));
+                float L = 0.0f;
+#pragma unroll 4
+                for (int c = tid / kRowsCols; c < seg.nsplit; c += per) {
+                    const float f = exp2f(fs[c * kRowsCols + g] - M);
+                    fs[c * kRowsCols + g] = f;
+                    L = fmaf(f, __ldcg(base(c) + kRowsCols * D + kRowsCols + g), L);
                 }
-                if (tid == 0) w.counters[s0] = 0;   // nobody arrives on it again in this call
+                L += __shfl_xor_sync(0xffffffffu, L, 8);
+                L += __shfl_xor_sync(0xffffffffu, L, 16);
+                if (lane < kRowsCols) lw[warp][lane] = L;
+                __syncthreads();
+                for (int i = tid; i < seg.cols * (D / 4); i += kRwThreads) {
+                    const int col = 4 * i / D;
+                    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                    for (int c = 0; c < seg.nsplit; ++c) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(base(c)) + i);
+                        const float f = fs[c * kRowsCols + col];
+                        O.x = fmaf(f, v.x, O.x), O.y = fmaf(f, v.y, O.y), O.z = fmaf(f, v.z, O.z), O.w = fmaf(f, v.w, O.w);
+                    }
+                    store_out(i, O, (lw[0][col] + lw[1][col]) + (lw[2][col] + lw[3][col]));
+                }
+                if (tid == 0) w.counters[c0] = 0;   // nobody arrives on it again in this call
             }
         }
-        if (piece + (int)gridDim.x >= pieces) return;
-        __syncthreads();   // the next piece's copies land where the merge wrote
+        __syncthreads();   // nobody reads the segment any more
+        if (tid == 0) {
+            RowsWork &wk = work_s;
+            wk.done += seg.count;
+            if (wk.done < wk.remaining) {   // a request that has rounds follows, if this one's items end
+                wk.offset = 0;
+                if (seg.last_item) {
+                    wk.item = 0;
+                    do ++wk.b;
+                    while (rows_rounds(p, wk.b) == 0);
+                } else {
+                    ++wk.item;
+                }
+            }
+        }
+        __syncthreads();
+        if (work_s.done == work_s.remaining) return;
     }
 }
 
@@ -822,9 +875,9 @@ cudaError_t launch(const RowsParams &w, cudaStream_t stream) {
 
 // Workspace: counters, partial results, the division of large batches.
 size_t rows_workspace_bytes(int64_t B, int64_t D) {
-    return (size_t)align256(4 * kRwSplitSlots) +
-           (size_t)align256(4 * (int64_t)kRwSplitSlots * (kRowsCols * D + 2 * kRowsCols)) +
-           (B > kRwWarpBatch ? (size_t)align256(8 * (B + 1)) : 0);
+    return (size_t)align256(4 * kRwResident) +
+           (size_t)align256(8 * (int64_t)kRwResident * (kRowsCols * D + 2 * kRowsCols)) +
+           (B > kRwWarpBatch ? (size_t)align256(8 * (B + 2)) : 0);
 }
 
 cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cudaStream_t stream) {
@@ -833,13 +886,13 @@ cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cud
     w.g_inv = (65536 + p.G - 1) / p.G;
     uint8_t *at = static_cast<uint8_t *>(ws);
     w.counters = reinterpret_cast<int32_t *>(at);
-    at += align256(4 * kRwSplitSlots);
+    at += align256(4 * kRwResident);
     w.part = reinterpret_cast<float *>(at);
-    at += align256(4 * (int64_t)kRwSplitSlots * (kRowsCols * D + 2 * kRowsCols));
-    w.division = nullptr;
+    at += align256(8 * (int64_t)kRwResident * (kRowsCols * D + 2 * kRowsCols));
+    w.first = nullptr;
     if (p.B > kRwWarpBatch) {
-        w.division = reinterpret_cast<int32_t *>(at);
-        kv4_rows_division_kernel<<<1, kDivThreads, 0, stream>>>(p, reinterpret_cast<int32_t *>(at));
+        w.first = reinterpret_cast<int64_t *>(at);
+        kv4_rows_division_kernel<<<1, kDivThreads, 0, stream>>>(p, reinterpret_cast<int64_t *>(at));
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
