@@ -458,7 +458,7 @@ qoq_status qoq_kv4_pages_release(const int32_t *leave, int64_t B, int64_t page_s
  * not).
  *
  * D 64 or 128; strides multiples of 8 and at least Hkv * D; k, v, codes and
- * outputs 16-byte aligned, params and slots 4-byte. N == 0 is a no-op.
+ * outputs 16-byte aligned, params 8-byte, slots 4-byte. N == 0 is a no-op.
  */
 qoq_status qoq_kv4_paged_write(const void *k_fp16, int64_t k_stride, const void *v_fp16, int64_t v_stride,
                                const int32_t *slots, int64_t N, int64_t Hkv, int64_t D, int64_t n_pages,
@@ -502,7 +502,7 @@ qoq_status qoq_kv4_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int6
  *
  * Hq a multiple of Hkv with Hq / Hkv <= 8, D 64 or 128; strides multiples of
  * 8 and at least Hq * D; window >= 0 (0: none), sinks >= 0 (no effect without
- * a window); q, codes and out 16-byte aligned, the rest 4-byte.
+ * a window); q, codes and out 16-byte aligned, params 8-byte, the rest 4-byte.
  * B at most 16384, Hkv at most 65535. N == 0 or B == 0 is a no-op.
  *
  * Workspace: as for qoq_kv4_decode_attention: size query with workspace ==

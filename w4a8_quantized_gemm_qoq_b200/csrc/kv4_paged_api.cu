@@ -98,7 +98,7 @@ qoq_status qoq_kv4_paged_write(const void *k_fp16, int64_t k_stride, const void 
         v_codes == nullptr || v_params == nullptr)
         return QOQ_ERR_INVALID_ARG;
     if (!aligned(k_fp16, 16) || !aligned(v_fp16, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
-        !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_params, 4) || !aligned(v_params, 4) ||
+        !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_params, 8) || !aligned(v_params, 8) ||
         !aligned(slots, 4))
         return QOQ_ERR_ALIGNMENT;
     return status_of(launch_paged_write(k_fp16, k_stride, v_fp16, v_stride, slots, N, Hkv, D, n_pages, shift, k_codes,
@@ -119,7 +119,7 @@ qoq_status qoq_kv4_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int6
     if (slots == nullptr || k_codes == nullptr || k_params == nullptr || v_codes == nullptr || v_params == nullptr ||
         k_out_fp16 == nullptr || v_out_fp16 == nullptr)
         return QOQ_ERR_INVALID_ARG;
-    if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_params, 4) || !aligned(v_params, 4) ||
+    if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_params, 8) || !aligned(v_params, 8) ||
         !aligned(slots, 4) || !aligned(k_out_fp16, 16) || !aligned(v_out_fp16, 16))
         return QOQ_ERR_ALIGNMENT;
     return status_of(launch_paged_read(slots, N, Hkv, D, n_pages, shift, k_codes, k_params, v_codes, v_params,
@@ -154,7 +154,7 @@ qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const u
         block_table == nullptr || q_start == nullptr || kv_lens == nullptr || out_fp16 == nullptr)
         return QOQ_ERR_INVALID_ARG;
     if (!aligned(q_fp16, 16) || !aligned(out_fp16, 16) || q_stride % 8 != 0 || out_stride % 8 != 0 ||
-        !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_params, 4) || !aligned(v_params, 4) ||
+        !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_params, 8) || !aligned(v_params, 8) ||
         !aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_lens, 4) || !aligned(workspace, 256))
         return QOQ_ERR_ALIGNMENT;
     PagedAttnParams p;

@@ -306,8 +306,8 @@ __device__ __forceinline__ void mma_16816_first(float (&c)[4], const uint32_t (&
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// NSUB: pages per 64-token tile (pages of 64 tokens or more: 1).
-template <int D, int NSUB>
+// SMALL: pages below 64 tokens, so that a tile has several.
+template <int D, bool SMALL>
 __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_constant__ RowsParams w) {
     constexpr int DB = D / 2;         // code bytes per vector
     constexpr int KW = DB / 16;       // K words a lane reads per token (bytes 4 KW tig .. 4 KW tig + 4 KW - 1)
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     __shared__ float mw[kRwWarps][kRowsCols], lw[kRwWarps][kRowsCols];
     __shared__ float mc[kRowsCols], lc[kRowsCols];
     __shared__ __align__(16) float2 kf_s[kRwWarps][kRwTile];   // per token: 2^24 s c, -z s c (c = log2(e) / sqrt(D))
-    __shared__ float vf_s[kRwWarps][kRwTile];                  // value scale * 2^(8 - E)
+    __shared__ __align__(16) float vf_s[kRwWarps][kRwTile];                  // value scale * 2^(8 - E)
     __shared__ __align__(16) __half vz_s[kRwWarps][kRwTile];   // value zero
     __shared__ int last_s;
     __shared__ RowsWork work_s;       // kept here and not in registers while the tiles are walked
@@ -337,12 +337,21 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     uint8_t *ring = rw_smem + (size_t)warp * 3 * TB;   // this warp's three tiles of codes, [64][DB] each
     const uint32_t ring_a = smem_u32(ring);
     __half *pt = reinterpret_cast<__half *>(rw_smem + (size_t)kRwWarps * 3 * TB) + warp * (kRwTile * 8);
-    // A lane copies the chunks lane + 32 i of a tile: chunk ck of token tk + (32 / CPT) i.
-    // Values are stored with a token's chunks permuted, so that the
-    // transposed loads of 8 tokens' same chunk touch every bank once.
-    const int tk = lane / CPT, ck = lane % CPT;
-    const uint32_t k_dst = (uint32_t)(lane * 16);
-    const uint32_t v_dst = (uint32_t)(tk * DB + ((ck ^ ((tk * CPT / 8) & (CPT - 1))) * 16));
+    // In small pages eight lanes copy the codes of 16 tokens, which lie in one
+    // page whatever its size: lane l the 16-byte chunks l % 8 + 8 i of the
+    // tile's tokens 16 (l / 8) .. + 15. Else a lane copies chunks l + 32 i:
+    // 512 bytes in a row per copy (the former costs 3% there, and saves 7% where
+    // four lookups and addresses per tile and lane are the alternative).
+    // Values are stored with a token's chunks permuted, so that the transposed
+    // loads of 8 tokens' same chunk touch every bank once: chunk c of token t is
+    // at c ^ (t / (8 / CPT)) % CPT, which is c ^ i % CPT in small pages and the same for every i else.
+    const int part = SMALL ? (lane >> 3) * 16 : 0;   // first token of the lane's page in a tile
+    // The two tokens whose factors it reads: neighbours, which share a small page, in one load; else two loads of a run.
+    const int tok0 = SMALL ? 2 * lane : lane, tok1 = SMALL ? 2 * lane + 1 : lane + 32;
+    const uint32_t src0 = (uint32_t)((SMALL ? lane & 7 : lane) * 16);
+    const uint32_t dst0 = (uint32_t)(part * DB) + src0;
+    const uint32_t swap = SMALL ? 0u : (uint32_t)((lane / 8) % CPT * 16);
+    constexpr int STEP = SMALL ? 128 : 512;
     // Every request with more rows than the caller promised is named.
     if (blockIdx.x == gridDim.x - 1)
         for (int b = tid; b < p.B; b += kRwThreads)
@@ -390,72 +399,67 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         auto tile_t0 = [&](int k) {
             return (k < tl.sink_tiles ? k : tl.first + (k - tl.sink_tiles)) * kRwTile;
         };
-        // The pages of tile k's parts: their numbers, or -1 past the
+        // The page of the lane's tokens of tile k: its number, or -1 past the
         // sequence's end and for numbers outside the cache.
         const int32_t *table = p.block_table + (int64_t)b * p.max_pages;
-        auto load_pages = [&](int k, int (&pg)[NSUB]) {
-            const int t = tile_t0(k);
-#pragma unroll
-            for (int i = 0; i < NSUB; ++i) {
-                pg[i] = -1;
-                if (k < k_end && t + i * (kRwTile / NSUB) < r.kv) {
-                    pg[i] = __ldg(table + ((t + i * (kRwTile / NSUB)) >> p.page_shift));
-                    if ((uint32_t)pg[i] >= (uint32_t)p.n_pages) {
-                        paged_bad_request(p, b);
-                        pg[i] = -1;
-                    }
+        auto load_page = [&](int k) {
+            const int t = tile_t0(k) + part;
+            int pg = -1;
+            if (k < k_end && t < r.kv) {
+                pg = __ldg(table + (t >> p.page_shift));
+                if ((uint32_t)pg >= (uint32_t)p.n_pages) {
+                    paged_bad_request(p, b);
+                    pg = -1;
                 }
             }
+            return pg;
         };
         // Tile k's codes into the ring at `dst` as one copy group (empty past
-        // the last tile). A part without a page copies page 0's codes, which
+        // the last tile). Tokens without a page copy page 0's codes, which
         // scales of 0 make nothing of; a page's tail past the sequence's end is in bounds.
-        auto issue = [&](int k, bool value, const int (&pg)[NSUB], uint32_t dst) {
+        auto issue = [&](int k, bool value, int pg, uint32_t dst) {
             if (k < k_end) {
-                const int in_page = tile_t0(k) & page_mask;
-                const uint8_t *base = p.k_codes + ((int64_t)h << p.page_shift) * DB + in_page * DB + lane * 16;
-                if (value) base += v_minus_k;
+                const uint32_t vec = ((uint32_t)h << p.page_shift) + (uint32_t)((tile_t0(k) + part) & page_mask);
+                const uint8_t *src = p.k_codes + ((uint64_t)(uint32_t)max(pg, 0) * page_vecs + vec) * DB + src0;
+                if (value) src += v_minus_k;
+                const uint32_t to = ring_a + dst + (value ? dst0 ^ swap : dst0);
 #pragma unroll
-                for (int i = 0; i < CPL; ++i) {
-                    constexpr int per = CPL / NSUB;   // a lane's copies per page
-                    const uint8_t *src = base + (uint64_t)(uint32_t)max(pg[i / per], 0) * (page_vecs * DB) + (i % per) * 512;
-                    copy16(ring_a + dst + (uint32_t)(i * 512) + (value ? v_dst : k_dst), src);
-                }
+                for (int i = 0; i < CPL; ++i)
+                    copy16((value && SMALL ? to ^ (uint32_t)((i % CPT) * 16) : to) + (uint32_t)(i * STEP), src + i * STEP);
             }
             copy_commit();
         };
-        // The tile's scales and zeros: token lane + 32 i in word i, as
-        // (scale | zero << 16); 0 past the sequence's end and on bad pages.
-        auto load_sz = [&](int k, const int (&pg)[NSUB], uint32_t (&kw)[2], uint32_t (&vw)[2]) {
-            const int t = tile_t0(k) + lane, in_page = (NSUB == 1 ? t - lane : 0) & page_mask;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                constexpr int part = kRwTile / NSUB;   // tokens per page of the tile (64, 32 or 16)
-                int page = pg[i * (NSUB / 2)];
-                int off = in_page + lane + 32 * i;
-                if (NSUB == 2) off = lane;
-                if (NSUB == 4) {
-                    page = lane < 16 ? pg[(2 * i) % NSUB] : pg[(2 * i + 1) % NSUB];
-                    off = lane & (part - 1);
-                }
-                kw[i] = vw[i] = 0u;
-                if (page >= 0 && t + 32 * i < r.kv) {
-                    const uint8_t *at = reinterpret_cast<const uint8_t *>(p.k_params) +
-                                        (((uint64_t)(uint32_t)page * page_vecs + ((uint32_t)h << p.page_shift) + off) << 2);
-                    kw[i] = __ldg(reinterpret_cast<const uint32_t *>(at));
-                    vw[i] = __ldg(reinterpret_cast<const uint32_t *>(at + vp_minus_kp));
+        // The scales and zeros of the lane's two tokens, (scale | zero << 16)
+        // each; 0 past the sequence's end and on bad pages.
+        auto load_sz = [&](int k, int pg, uint32_t (&kw)[2], uint32_t (&vw)[2]) {
+            const int t = tile_t0(k);
+            kw[0] = kw[1] = vw[0] = vw[1] = 0u;
+            if (pg < 0 || t + tok0 >= r.kv) return;
+            const uint32_t vec = ((uint32_t)h << p.page_shift) + (SMALL ? (uint32_t)((t + tok0) & page_mask) : (uint32_t)((t & page_mask) + tok0));
+            const uint8_t *at = reinterpret_cast<const uint8_t *>(p.k_params) +
+                                (((uint64_t)(uint32_t)pg * page_vecs + vec) << 2);
+            if (SMALL) {
+                const uint2 kk = __ldg(reinterpret_cast<const uint2 *>(at));
+                const uint2 vv = __ldg(reinterpret_cast<const uint2 *>(at + vp_minus_kp));
+                kw[0] = kk.x, vw[0] = vv.x;
+                if (t + tok1 < r.kv) kw[1] = kk.y, vw[1] = vv.y;
+            } else {
+                kw[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+                vw[0] = __ldg(reinterpret_cast<const uint32_t *>(at + vp_minus_kp));
+                if (t + tok1 < r.kv) {
+                    kw[1] = __ldg(reinterpret_cast<const uint32_t *>(at + 128));
+                    vw[1] = __ldg(reinterpret_cast<const uint32_t *>(at + 128 + vp_minus_kp));
                 }
             }
         };
 
         int k = k_begin + warp;
         uint32_t s0 = 0, s1 = TB, s2 = 2 * TB;   // ring places of this tile's keys and values and the next tile's keys
-        int pgn[NSUB];
+        int pgn;
         uint32_t kw[2] = {0u, 0u}, vw[2] = {0u, 0u};
         {
-            int pg[NSUB];
-            load_pages(k, pg);
-            load_pages(k + kRwWarps, pgn);
+            const int pg = load_page(k);
+            pgn = load_page(k + kRwWarps);
             issue(k, false, pg, s0);
             issue(k, true, pg, s1);
             if (k < k_end) load_sz(k, pg, kw, vw);
@@ -525,8 +529,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
 
         for (; k < k_end; k += kRwWarps) {
             const int t0 = tile_t0(k);
-            int pgnn[NSUB];
-            load_pages(k + 2 * kRwWarps, pgnn);
+            const int pgnn = load_page(k + 2 * kRwWarps);
             uint32_t kwn[2] = {0u, 0u}, vwn[2] = {0u, 0u};
             if (k + kRwWarps < k_end) load_sz(k + kRwWarps, pgn, kwn, vwn);   // in flight while this tile is computed
             // Whether every column sees every token of the tile.
@@ -544,10 +547,11 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             __syncwarp();   // every lane is done with the last tile's factors
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                const int t = i ? tok1 : tok0;
                 const float s = half_lo(kw[i]) * p.qscale;
-                kf_s[warp][lane + 32 * i] = make_float2(s * 0x1p24f, -__half2float(half_hi(kw[i])) * s);
-                vf_s[warp][lane + 32 * i] = half_lo(vw[i]) * ef;
-                vz_s[warp][lane + 32 * i] = half_hi(vw[i]);
+                kf_s[warp][t] = make_float2(s * 0x1p24f, -__half2float(half_hi(kw[i])) * s);
+                vf_s[warp][t] = half_lo(vw[i]) * ef;
+                vz_s[warp][t] = half_hi(vw[i]);
             }
             copy_wait<2>();   // this tile's keys have landed
             __syncwarp();
@@ -703,8 +707,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             const uint32_t s = s0;
             s0 = s2, s2 = s1, s1 = s;
             kw[0] = kwn[0], kw[1] = kwn[1], vw[0] = vwn[0], vw[1] = vwn[1];
-#pragma unroll
-            for (int i = 0; i < NSUB; ++i) pgn[i] = pgnn[i];
+            pgn = pgnn;
         }
         copy_wait<0>();
 
@@ -851,24 +854,23 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     }
 }
 
-template <int D, int NSUB>
+template <int D, bool SMALL>
 cudaError_t launch(const RowsParams &w, cudaStream_t stream) {
     // Per warp, three 64-token tiles of codes, then the P tiles (1 KB per
     // warp): 52 KB at D = 128, four CTAs per SM.
     constexpr int smem = kRwWarps * 3 * kRwTile * D / 2 + kRwWarps * kRwTile * 8 * 2;
     if (smem > 40 * 1024) {
         static SmemOptIn opt_in;
-        const cudaError_t e = opt_in.set(kv4_rows_kernel<D, NSUB>, smem);
+        const cudaError_t e = opt_in.set(kv4_rows_kernel<D, SMALL>, smem);
         if (e != cudaSuccess) return e;
     }
-    kv4_rows_kernel<D, NSUB><<<kRwResident, kRwThreads, smem, stream>>>(w);
+    kv4_rows_kernel<D, SMALL><<<kRwResident, kRwThreads, smem, stream>>>(w);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch(const RowsParams &w, cudaStream_t stream) {
-    return w.a.page_shift >= 6 ? launch<D, 1>(w, stream)
-                               : (w.a.page_shift == 5 ? launch<D, 2>(w, stream) : launch<D, 4>(w, stream));
+    return w.a.page_shift >= 6 ? launch<D, false>(w, stream) : launch<D, true>(w, stream);
 }
 
 }  // namespace
