@@ -30,6 +30,36 @@ __device__ __forceinline__ void paged_bad_request(const PagedAttnParams &p, int 
     if (atomicCAS(p.status, 0, QOQ_ERR_INVALID_ARG) == 0) p.status[1] = b;
 }
 
+// Pairs of FP32 values, for the operations that take two at once.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    return pair_of(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 of_pair(uint64_t v) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Opts a kernel in to more than 48 KB of dynamic shared memory, once per device.
 struct SmemOptIn {
     std::atomic<uint64_t> done{0};   // devices 0 .. 63, a bit each

@@ -59,73 +59,87 @@ __device__ __forceinline__ float quotient(float a, float b, float y) {
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 
-// Vector index -> row and head; returns the slot's place in the cache ((page
-// * Hkv + head) * page_size + offset), or -1 for a row without a slot.
-__device__ __forceinline__ int64_t vector_of(const PagedCacheParams &p, uint32_t vec, uint32_t &row, uint32_t &h) {
-    row = vec / (uint32_t)p.Hkv;
-    h = vec - row * (uint32_t)p.Hkv;
-    const int slot = __ldg(p.slots + row);
-    if ((uint32_t)slot >= (uint32_t)p.n_slots) return -1;
-    const int64_t page = slot >> p.page_shift;
-    return ((page * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+// A CTA takes one head of PER x VPC rows (so that the codes and parameters of
+// neighbouring tokens, neighbours in a page, are stored together), a thread of
+// the rows `row`, row + VPC, ...
+template <int VPC, int PER>
+__device__ __forceinline__ void vectors_of(const PagedCacheParams &p, int64_t &row, int &h) {
+    const uint32_t block = blockIdx.x / (uint32_t)p.Hkv;
+    h = (int)(blockIdx.x - block * (uint32_t)p.Hkv);
+    row = (int64_t)block * (PER * VPC) + threadIdx.x / (kPcThreads / VPC);
 }
 
-// PER: vectors per thread, PER spans of a CTA's width apart.
+// The place of a slot's vector of head h in the cache, (page * Hkv + head) *
+// page_size + offset, or -1 for a row that has none.
+__device__ __forceinline__ int64_t place_of(const PagedCacheParams &p, int64_t row, int h) {
+    if (row >= p.N) return -1;
+    const int slot = __ldg(p.slots + row);
+    if ((uint32_t)slot >= (uint32_t)p.n_slots) return -1;
+    return (((int64_t)(slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+}
+
 template <int D, int PER>
 __global__ void __launch_bounds__(kPcThreads) kv4_paged_write_kernel(const __grid_constant__ PagedCacheParams p) {
-    constexpr int LPV = D / 8, VPC = kPcThreads / LPV;   // lanes per vector, vectors per CTA and span
+    constexpr int LPV = D / 8, VPC = kPcThreads / LPV;   // lanes per vector, vectors per CTA and turn
     const int l = threadIdx.x % LPV;
     const bool is_v = blockIdx.y != 0;
-    const __half *from = is_v ? p.v : p.k;
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    const uint32_t n = (uint32_t)(p.N * p.Hkv), vec0 = blockIdx.x * (PER * VPC) + threadIdx.x / LPV;
+    int64_t row;
+    int h;
+    vectors_of<VPC, PER>(p, row, h);
+    const uint4 *from = reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + row * stride + h * D) + l;
     int64_t at[PER];
     uint4 u[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const uint32_t vec = vec0 + i * VPC;
-        uint32_t row, h;
-        at[i] = -1;
         u[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (vec < n) {
-            at[i] = vector_of(p, vec, row, h);
-            u[i] = __ldg(reinterpret_cast<const uint4 *>(from + row * stride + h * D) + l);
-        }
+        if (row + i * VPC < p.N) u[i] = __ldg(from + i * (VPC * stride / 8));
+        at[i] = place_of(p, row + i * VPC, h);
     }
+    __half2 mine;   // (-lo, hi) of the vector l % PER
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        // (-lo, hi) of the lane's 8 values, then of the vector's lanes; a NaN counts for neither.
-        const __half2 mn = __hmin2(__hmin2(as_half2(w[0]), as_half2(w[1])), __hmin2(as_half2(w[2]), as_half2(w[3])));
-        const __half2 mx = __hmax2(__hmax2(as_half2(w[0]), as_half2(w[1])), __hmax2(as_half2(w[2]), as_half2(w[3])));
-        const __half2 nm = __hneg2(mn);
+        const __half2 a = as_half2(u[i].x), b = as_half2(u[i].y), c = as_half2(u[i].z), d = as_half2(u[i].w);
+        // Of the lane's 8 values, then of the vector's lanes; a NaN counts for neither.
+        const __half2 nm = __hneg2(__hmin2(__hmin2(a, b), __hmin2(c, d))), mx = __hmax2(__hmax2(a, b), __hmax2(c, d));
         __half2 ext = __hmax2(__hmax2(__lows2half2(nm, mx), __highs2half2(nm, mx)), __floats2half2_rn(0.0f, 0.0f));
 #pragma unroll
         for (int o = LPV / 2; o > 0; o >>= 1)   // the whole warp takes part
             ext = __hmax2(ext, as_half2(__shfl_xor_sync(0xffffffffu, half2_bits(ext), o)));
+        if (i == 0 || l % PER == i) mine = ext;
+    }
+    // A lane works out one vector's scale, its reciprocal and the zero.
+    const float neg_lo = __low2float(mine);
+    const __half sh = __float2half_rn(__fdiv_rn(__fadd_rn(__high2float(mine), neg_lo), 15.0f));
+    const float scale = __half2float(sh), rcp = __frcp_rn(scale);
+    const __half zh = __int2half_rn(scale != 0.0f ? (int)rintf(quotient(neg_lo, scale, rcp)) : 0);
+    const uint32_t param = half2_bits(__halves2half2(sh, zh));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const uint32_t sz = __shfl_sync(0xffffffffu, param, i, LPV);
+        const float y = __shfl_sync(0xffffffffu, rcp, i, LPV);
         if (at[i] < 0) continue;
-        const float neg_lo = __low2float(ext);
-        const __half sh = __float2half_rn(__fdiv_rn(__fadd_rn(__high2float(ext), neg_lo), 15.0f));
-        const float s = __half2float(sh);
-        float zf = 0.0f;
+        const float s = half_lo(sz), zf = __half2float(half_hi(sz));
         uint32_t codes = 0u;
         if (s != 0.0f) {
-            const float y = __frcp_rn(s);
-            zf = rintf(quotient(neg_lo, s, y));
-            // The sum's bits are those of 1.5 * 2^23 plus the code: the former's share of the shifted sum goes last.
-            constexpr uint32_t base = 0x4B400000u;
+            const uint64_t y2 = pair_of(y, y), s2 = pair_of(-s, -s), z2 = pair_of(zf, zf);
+            const uint64_t round2 = pair_of(kRoundInt, kRoundInt);
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            // A sum's bits are those of 1.5 * 2^23 plus the code: the former's share of the shifted sum goes last.
             uint32_t shares = 0u;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = e % 2 ? __high2float(as_half2(w[e / 2])) : __low2float(as_half2(w[e / 2]));
-                const float r = __fadd_rn(__fadd_rn(quotient(x, s, y), kRoundInt), zf);
-                codes += __float_as_uint(fminf(fmaxf(r, kRoundInt), kRoundInt + 15.0f)) << (4 * e);   // NaN: 0
-                shares += base << (4 * e);
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = __half22float2(as_half2(w[e]));
+                const uint64_t x2 = pair_of(x.x, x.y), q = mul2(x2, y2);
+                const float2 r = of_pair(add2(add2(fma2(fma2(q, s2, x2), y2, q), round2), z2));   // Markstein's, as above
+                codes += __float_as_uint(fminf(fmaxf(r.x, kRoundInt), kRoundInt + 15.0f)) << (8 * e);   // NaN: 0
+                codes += __float_as_uint(fminf(fmaxf(r.y, kRoundInt), kRoundInt + 15.0f)) << (8 * e + 4);
+                shares += 0x4B400000u * 17u << (8 * e);
             }
             codes -= shares;
         }
         reinterpret_cast<uint32_t *>(is_v ? p.v_codes : p.k_codes)[at[i] * LPV + l] = codes;
-        if (l == 0) (is_v ? p.v_params : p.k_params)[at[i]] = __halves2half2(sh, __int2half_rn((int)zf));
+        if (l == i) (is_v ? p.v_params : p.k_params)[at[i]] = as_half2(sz);
     }
 }
 
@@ -134,33 +148,36 @@ __global__ void __launch_bounds__(kPcThreads) kv4_paged_read_kernel(const __grid
     constexpr int LPV = D / 8, VPC = kPcThreads / LPV;
     const int l = threadIdx.x % LPV;
     const bool is_v = blockIdx.y != 0;
-    const uint32_t *codes = reinterpret_cast<const uint32_t *>(is_v ? p.v_codes : p.k_codes);
+    const uint32_t *codes = reinterpret_cast<const uint32_t *>(is_v ? p.v_codes : p.k_codes) + l;
     const uint32_t *params = reinterpret_cast<const uint32_t *>(is_v ? p.v_params : p.k_params);
-    const uint32_t n = (uint32_t)(p.N * p.Hkv), vec0 = blockIdx.x * (PER * VPC) + threadIdx.x / LPV;
+    int64_t row;
+    int h;
+    vectors_of<VPC, PER>(p, row, h);
+    uint4 *to = reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out) + (row * p.Hkv + h) * LPV + l;
     int64_t at[PER];
     uint32_t c[PER], sz[PER];
 #pragma unroll
+    for (int i = 0; i < PER; ++i) at[i] = place_of(p, row + i * VPC, h);
+#pragma unroll
     for (int i = 0; i < PER; ++i) {
-        uint32_t row, h;
-        at[i] = vec0 + i * VPC < n ? vector_of(p, vec0 + i * VPC, row, h) : -1;
+        c[i] = sz[i] = 0u;
+        if (at[i] >= 0) {
+            c[i] = __ldg(codes + at[i] * LPV);
+            sz[i] = __ldg(params + at[i]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        c[i] = at[i] >= 0 ? __ldg(codes + at[i] * LPV + l) : 0u;
-        sz[i] = at[i] >= 0 ? __ldg(params + at[i]) : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (vec0 + i * VPC >= n) continue;
-        const __half2 s = __half2half2(__low2half(as_half2(sz[i])));
-        const __half2 z = __hadd2(__half2half2(__high2half(as_half2(sz[i]))), __floats2half2_rn(1024.0f, 1024.0f));
+        if (row + i * VPC >= p.N) break;
+        const __half2 s = __low2half2(as_half2(sz[i]));
+        const __half2 z = __hadd2(__high2half2(as_half2(sz[i])), __floats2half2_rn(1024.0f, 1024.0f));
         uint32_t r[4];   // codes e and e + 4 in r[e]
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t q = (c[i] >> (4 * e) & 0x000F000Fu) | 0x64006400u;
             r[e] = half2_bits(__hmul2(__hsub2(as_half2(q), z), s));
         }
-        reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out)[(int64_t)(vec0 + i * VPC) * LPV + l] =
+        to[(int64_t)i * VPC * p.Hkv * LPV] =
             make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
                        __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
     }
@@ -168,8 +185,8 @@ __global__ void __launch_bounds__(kPcThreads) kv4_paged_read_kernel(const __grid
 
 template <int D, int PER>
 cudaError_t launch(const PagedCacheParams &p, bool write, cudaStream_t stream) {
-    constexpr int VPC = PER * (kPcThreads / (D / 8));   // vectors per CTA
-    const dim3 grid((unsigned)((p.N * p.Hkv + VPC - 1) / VPC), 2);
+    constexpr int rows = PER * kPcThreads / (D / 8);   // per CTA
+    const dim3 grid((unsigned)((p.N + rows - 1) / rows * p.Hkv), 2);
     if (write)
         kv4_paged_write_kernel<D, PER><<<grid, kPcThreads, 0, stream>>>(p);
     else

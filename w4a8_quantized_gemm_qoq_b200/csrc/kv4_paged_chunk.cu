@@ -287,35 +287,6 @@ __device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint32_t b, 
 }
 
 // Two FP32 values in one register pair, each operation on both.
-__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-    return pair_of(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ float2 of_pair(uint64_t v) {
-    uint32_t lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // The accesses below are warp-collective: the warp must be converged.
 //
 // Loads of 16 lanes x 32 columns in the layout of matrix fragments: lane t's
