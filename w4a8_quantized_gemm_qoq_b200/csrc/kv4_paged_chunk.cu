@@ -32,6 +32,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kv4_mma.cuh"
 #include "kv4_paged.cuh"
 #include "qoq_device.cuh"
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __
         }
     }
     if (threadIdx.x == 0) w.division[p.B] = base0, w.division[2 * p.B + 1] = base1;
+    griddep_wait();   // the few-rows kernel: what waits for this one waits for both
 }
 
 // ------------------------------------------------------------ tensor cores
@@ -1104,6 +1107,7 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_consta
     const PagedAttnParams &p = w.a;
     griddep_wait();   // the parts
     const int slots = w.division[2 * p.B + 1], turns = w.slot_rows / kJoinRows;
+    using Row = typename std::conditional<D == 128, float4, float2>::type;   // a lane's dims
     const int lane = threadIdx.x & 31;
     const float2 *ml = reinterpret_cast<const float2 *>(w.part + (int64_t)kChSlots * w.slot_rows * D);
 #pragma unroll 1
@@ -1116,21 +1120,32 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_consta
         const int rows = min(min(r.n * p.G - it.z * kChRows, kChRows), row0 + kJoinRows);
 #pragma unroll 1
         for (int row = row0 + (threadIdx.x >> 5); row < rows; row += 8) {
+            // Lane i holds part i's maximum and weight (then i + 32's, ...).
             float m = -INFINITY, l = 0.0f, o[D / 32];
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
 #pragma unroll 1
-            for (int i = 0; i < parts; ++i) m = fmaxf(m, ml[(int64_t)(slot + i) * w.slot_rows + row].x);
-#pragma unroll 2
-            for (int i = 0; i < parts; ++i) {
-                const int64_t at = (int64_t)(slot + i) * w.slot_rows + row;
-                const float2 x = ml[at];
-                const float f = x.y > 0.0f ? exp2f(x.x - m) : 0.0f;
-                l += f * x.y;
-                const float *src = w.part + at * D + lane * (D / 32);
+            for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[(int64_t)(slot + i) * w.slot_rows + row].x);
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, src[e], o[e]);
+            for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+#pragma unroll 1
+            for (int i0 = 0; i0 < parts; i0 += 32) {
+                const float2 x = i0 + lane < parts ? ml[(int64_t)(slot + i0 + lane) * w.slot_rows + row] : make_float2(0.0f, 0.0f);
+                const float mine = x.y > 0.0f ? exp2f(x.x - m) : 0.0f;
+                l = fmaf(mine, x.y, l);
+                const float *src = w.part + ((int64_t)(slot + i0) * w.slot_rows + row) * D + lane * (D / 32);
+                const int n = min(parts - i0, 32);
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) {
+                    const float f = __shfl_sync(0xffffffffu, mine, i);
+                    Row v = *reinterpret_cast<const Row *>(src + (int64_t)i * w.slot_rows * D);
+                    const float *x4 = reinterpret_cast<const float *>(&v);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(f, x4[e], o[e]);
+                }
             }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
             const float f = l > 0.0f ? 1.0f / l : 0.0f;
             const int pair = it.z * kChRows + row, token = pair / p.G;
             __half2 *out = reinterpret_cast<__half2 *>(p.out + (int64_t)(r.row0 + token) * p.out_stride +
@@ -1149,7 +1164,8 @@ int slot_rows(int64_t max_new, int64_t G) {
 // A launch that may begin before the kernel ahead of it has ended, whose results
 // it waits for itself.
 template <typename Kernel>
-cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, const ChunkParams &w, cudaStream_t stream) {
+cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, const ChunkParams &w, cudaStream_t stream,
+                             bool dependent = true) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
@@ -1159,7 +1175,7 @@ cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, c
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, w);
 }
 
@@ -1170,8 +1186,9 @@ cudaError_t launch(const ChunkParams &w, cudaStream_t stream) {
     cudaError_t e = opt_in.set(kv4_chunk_kernel<D>, smem);
     if (e != cudaSuccess) return e;
     const int threads = w.a.B >= kDvThreads ? kDvThreads : (w.a.B + 31) / 32 * 32;
-    kv4_chunk_division_kernel<<<1, threads, 0, stream>>>(w);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // Beside the few-rows kernel, where that runs: it reads nothing that one writes.
+    e = launch_dependent(kv4_chunk_division_kernel, 1, threads, 0, w, stream, w.rows_limit > 0);
+    if (e != cudaSuccess) return e;
     e = launch_dependent(kv4_chunk_kernel<D>, kChCtas, kChThreads, smem, w, stream);
     if (e != cudaSuccess) return e;
     return launch_dependent(kv4_chunk_join_kernel<D>, kJoinCtas, 256, 0, w, stream);

@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     __shared__ RowsWork work_s;       // kept here and not in registers while the tiles are walked
     __shared__ RowsSegment seg_s;
 
+    griddep_launch_dependents();   // the many-rows kernel's division
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
     uint8_t *ring = rw_smem + (size_t)warp * 3 * TB;   // this warp's three tiles of codes, [64][DB] each
