@@ -379,6 +379,14 @@ def _stream_scope(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _empty_fp16(shape, device, stream):
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=torch.float16, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=torch.float16, device=device)
+
+
 def _i32(t, shape, device, name):
     """Pointer of an int32 CUDA tensor of this shape on this device."""
     import torch
@@ -585,14 +593,13 @@ class PagedKV4Cache:
         N = slots.shape[0]
         sp = _i32(slots, (N,), device, "slots")
         shape = (N, self.Hkv, self.D)
-        if k is None or v is None:
-            with _stream_scope(stream):
-                k = torch.empty(shape, dtype=torch.float16, device=device) if k is None else k
-                v = torch.empty(shape, dtype=torch.float16, device=device) if v is None else v
         for t, name in ((k, "k"), (v, "v")):
-            _cuda_tensor(t, torch.float16, name)
-            if t.shape != shape or t.device != device:
-                raise ValueError("%s must have shape %s on %s" % (name, shape, device))
+            if t is not None:
+                _cuda_tensor(t, torch.float16, name)
+                if t.shape != shape or t.device != device:
+                    raise ValueError("%s must have shape %s on %s" % (name, shape, device))
+        k = _empty_fp16(shape, device, stream) if k is None else k
+        v = _empty_fp16(shape, device, stream) if v is None else v
         code = lib().qoq_kv4_paged_read(sp, N, *self._sizes, *self._ptrs, _vp(k.data_ptr()), _vp(v.data_ptr()),
                                         _raw_stream(stream, device.index))
         if code:
@@ -624,12 +631,11 @@ def kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window
     N, Hq = q.shape[0], q.shape[1]
     qp, qs = _rows(q, Hq, cache.D, device, "q")
     B, max_pages = block_table.shape
-    if ws is None or out is None:
+    if ws is None:
         with _stream_scope(stream):
-            if ws is None:
-                ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, cache.D, max_new), device)
-            if out is None:
-                out = torch.empty((N, Hq, cache.D), dtype=torch.float16, device=device)
+            ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, cache.D, max_new), device)
+    if out is None:
+        out = _empty_fp16((N, Hq, cache.D), device, stream)
     op, os_ = _rows(out, Hq, cache.D, device, "out")
     if out.shape[0] != N or ws.buf.device != device:
         raise ValueError("out must have q's shape, and the workspace its device")
