@@ -249,7 +249,7 @@ def test_decode(Hq, Hkv, D, page):
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)
-@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("page", [16, 32, 128, 256])
 def test_chunks(Hq, Hkv, D, page):
     """Ragged new tokens over ragged contexts, requests without rows or
     tokens among them; rows behind the last stay."""
@@ -424,6 +424,112 @@ def test_one_graph_for_growing_sequences():
         o = host(out)
         assert (o[a.rows:] == 7.0).all() and ws.status() == 0
         check(a, o)
+
+
+@pytest.mark.parametrize("G,Hkv,D", [(1, 2, 128), (3, 1, 64), (8, 2, 64), (7, 1, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 70)])
+def test_rows_around_eight_and_thirty_two_pairs(G, Hkv, D, window, sinks):
+    """Row counts at which a KV head's (row, head) pairs pass a multiple of 8, or 32."""
+    new = sorted({max(1, n // G + d) for n in (8, 16, 24, 32) for d in (0, 1)})
+    b = Batch([(0, 61, 500, 3, 260, 1000)[i % 6] for i in range(len(new))], new, G * Hkv, Hkv, D, 16, seed=G)
+    check(b, run(b, window, sinks), window, sinks)
+
+
+@pytest.mark.parametrize("B,Hkv,D,top", [(129, 1, 64, 70), (140, 8, 64, 40), (300, 2, 128, 0), (592, 1, 64, 0),
+                                         (593, 1, 64, 0), (1100, 1, 64, 50), (2100, 1, 64, 20)])
+@pytest.mark.parametrize("chunks", [False, True])
+def test_large_batches(B, Hkv, D, top, chunks):
+    """Batches whose division is worked out by a kernel of its own, of equal
+    (top 0) and ragged lengths, with and without requests of many rows."""
+    rng = np.random.default_rng(B)
+    ctx = rng.integers(0, top, B) if top else np.full(B, 33)
+    new = np.ones(B, int)
+    if chunks:
+        new[::B // 7] = rng.integers(9, 50, len(new[::B // 7]))
+        new[5::97] = 0
+    b = Batch(ctx, new, 4 * Hkv, Hkv, D, 16, seed=B, spare_rows=2)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,page", [
+    ([40000], [1], 1, 1, 64, 256), ([200000], [1], 2, 1, 64, 256), ([9000], [5], 8, 2, 128, 16),
+    ([1] * 40 + [30000], [1] * 41, 4, 2, 64, 64), ([20000, 0, 0, 3, 5000], [1, 1, 0, 2, 1], 4, 1, 128, 32),
+    ([30000, 10], [40, 90], 4, 1, 64, 128)])
+def test_long_sequences_among_short_ones(ctx, new, Hq, Hkv, D, page):
+    """Sequences that many CTAs share, alone and beside short ones."""
+    b = Batch(ctx, new, Hq, Hkv, D, page, seed=len(ctx))
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    B, Hkv, D = int(rng.integers(1, 40)), int(rng.choice([1, 2, 3, 8])), int(rng.choice([64, 128]))
+    G, page = int(rng.integers(1, 9)), int(rng.choice([16, 32, 64, 128, 256]))
+    ctx = np.exp(rng.uniform(0, np.log(3000), B)).astype(int) - 1
+    new = np.where(rng.random(B) < 0.6, 1, rng.integers(0, 70, B))
+    window, sinks = ((0, 0), (int(rng.integers(1, 700)), int(rng.integers(0, 90))))[seed % 2]
+    b = Batch(ctx, new, G * Hkv, Hkv, D, page, seed=seed, spare_rows=1)
+    check(b, run(b, window, sinks), window, sinks)
+
+
+def test_pages_beyond_four_gigabytes():
+    """Codes at offsets past 32 bits: the last pages of a cache of 4.3 GB per
+    tensor are written, read and attended to."""
+    t = torch()
+    n_pages, Hkv, P, D = 33000, 8, 256, 128
+    c = qoq.PagedKV4Cache(n_pages, Hkv, P, D)
+    assert c.k_codes.numel() > 2 ** 32
+    rng = np.random.default_rng(22)
+    ctx = [600, 300]
+    table = np.array([[32999, 5, 32990], [32800, 32801, -1]], np.int32)
+    kv = rng.standard_normal((2, sum(ctx), Hkv, D)).astype(np.float16)
+    at = [np.arange(n) for n in ctx]
+    slots = np.concatenate([table[r, a // P] * P + a % P for r, a in enumerate(at)]).astype(np.int32)
+    c.write(dev(kv[0]), dev(kv[1]), dev(slots))
+    k, v = c.read(dev(slots))
+    for x, got in zip(kv, (k, v)):
+        d = kv4_paged.quantize_kv4(x)
+        want = ((d["q"].astype(np.float32) - d["z"].astype(np.float32)[..., None]) * d["s"].astype(np.float32)[..., None])
+        assert (host(got) == want.astype(np.float16)).all()
+    # The oracle on the same pages, renumbered.
+    pages = [32999, 5, 32990, 32800, 32801]
+    small = [host(x[pages]) for x in (c.k_codes, c.k_params, c.v_codes, c.v_params)]
+    small_table = np.array([[0, 1, 2], [3, 4, -1]], np.int32)
+    for new in ([1, 1], [70, 3]):
+        q_start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q = rng.standard_normal((q_start[-1], 16, D)).astype(np.float16)
+        out = host(qoq.kv4_paged_attention(dev(q), c, dev(table), dev(q_start), dev(np.array(ctx, np.int32)), max(new)))
+        o, vmax = kv4_paged.attention(q, *small, small_table, q_start, np.array(ctx, np.int32), 0, 0)
+        assert (np.abs(out - o).max(axis=2) <= 2.0 ** -10 * vmax + 2.0 ** -24).all()
+    del c, k, v
+    t.cuda.empty_cache()
+
+
+def test_a_step_on_a_given_stream():
+    """Plan, write, read, attention and release with stream=: the buffers and
+    bits of the same calls on the current stream."""
+    t = torch()
+    rng = np.random.default_rng(23)
+    new, rows = dev(np.array([70, 0, 3, 200], np.int32)), rng.standard_normal((2, 280, 2, 64)).astype(np.float16)
+    q = dev(rng.standard_normal((280, 8, 64)).astype(np.float16))
+    leave = dev(np.array([0, 0, 1, 1], np.int32))
+    got = []
+    for s in (None, t.cuda.Stream()):
+        pt, c, step = qoq.PageTable(4, 20, 40, 16), qoq.PagedKV4Cache(40, 2, 16, 64), qoq.PagedStep(4, 280)
+        k, v = dev(rows[0]), dev(rows[1])
+        out, kr, vr = t.zeros_like(q), t.zeros_like(k), t.zeros_like(v)
+        ws = qoq.Workspace(qoq.kv4_paged_workspace_bytes(4, 280, 8, 2, 64, 200))
+        t.cuda.synchronize()
+        pt.assign(new, step, stream=s)
+        c.write(k, v, step.slots, stream=s)
+        assert c.read(step.slots, kr, vr, stream=s) == (kr, vr)
+        qoq.kv4_paged_attention(q, c, pt.block_table, step.q_start, pt.seq_lens, 200, ws=ws, out=out, stream=s)
+        pt.release(leave, stream=s)
+        t.cuda.synchronize()
+        assert pt.status() == 0 and ws.status() == 0 and host(pt.seq_lens).tolist() == [70, 0, 0, 0]
+        got.append([host(x) for x in (out, kr, vr, step.slots, pt.block_table, pt.free_pages)])
+    assert all(np.array_equal(a, b) for a, b in zip(*got)) and (got[0][1][:273] != 0).any()
 
 
 def test_strided_queries_and_outputs():

@@ -118,7 +118,7 @@ def test_paged_cache_calls_refuse(L):
 
     assert write(D=96) == 2 and write(H=0) == 1 and write(H=70000, ks=1 << 24, vs=1 << 24) == 2 and write(N=-1) == 1
     assert write(ks=1016) == 1 and write(vs=0) == 1 and write(page=20) == 2 and write(n=-3) == 1
-    assert write(ks=1028) == 3 and write(k=P16 + 8) == 3 and write(c=P16 + 4) == 3 and write(m=P16 + 2) == 3
+    assert write(ks=1028) == 3 and write(k=P16 + 8) == 3 and write(c=P16 + 4) == 3 and write(m=P16 + 4) == 3
     assert write(slots=P16 + 1) == 3 and write(k=None) == 1 and write(slots=None) == 1 and write(c=None) == 1
     assert write(N=0, k=None, v=None, slots=None) == 0
 
@@ -144,7 +144,7 @@ def test_paged_attention_refuses(L):
     for name in ("q", "c", "m", "table", "q_start", "kv", "out"):
         assert call(**{name: None}) == 1, name
         assert call(**{name: P16 + 2}) == 3, name
-    assert call(q=P16 + 8) == 3 and call(qs=4100) == 3 and call(os=4100) == 3 and call(ws=P16 + 128) == 3
+    assert call(q=P16 + 8) == 3 and call(qs=4100) == 3 and call(os=4100) == 3 and call(ws=P16 + 128) == 3 and call(m=P16 + 4) == 3
     assert call(B=0, q=None) == 0 and call(N=0, q=None) == 0
     assert qoq.kv4_paged_workspace_bytes(64, 64, 32, 8, 128, 1) >= 256
 
