@@ -507,7 +507,11 @@ qoq_status qoq_kv4_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int6
  *
  * Workspace: as for qoq_kv4_decode_attention: size query with workspace ==
  * NULL, 256-byte aligned, zero-filled before its first use, status words in
- * bytes [0, 256) ([0] the code; with QOQ_ERR_INVALID_ARG [1] = the request),
+ * bytes [0, 256) ([0] stays 0 or becomes a code that the caller clears; with
+ * QOQ_ERR_INVALID_ARG [1] = the request; with QOQ_ERR_TIMEOUT [1] = the wait
+ * that ran out after 1 s, 20 for queries, 21 keys, 22 values, 23 weights, 24
+ * scores, 25 outputs, 26 a free stage, [2] = the CTA, [3] = its step or
+ * piece, and the outputs are undefined),
  * control words that every call leaves zero, then scratch; calls that may
  * overlap on the device need separate workspaces. The size depends on B, N,
  * the heads and max_new, not on the lengths.

@@ -428,9 +428,9 @@ def test_one_graph_for_growing_sequences():
 
 @pytest.mark.parametrize("G,Hkv,D", [(1, 2, 128), (3, 1, 64), (8, 2, 64), (7, 1, 128)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 70)])
-def test_rows_around_eight_and_thirty_two_pairs(G, Hkv, D, window, sinks):
-    """Row counts at which a KV head's (row, head) pairs pass a multiple of 8, or 32."""
-    new = sorted({max(1, n // G + d) for n in (8, 16, 24, 32) for d in (0, 1)})
+def test_rows_around_the_kernels_limits(G, Hkv, D, window, sinks):
+    """Row counts at which a KV head's (row, head) pairs pass a multiple of 8, or 48."""
+    new = sorted({max(1, n // G + d) for n in (8, 16, 24, 40, 48) for d in (0, 1)})
     b = Batch([(0, 61, 500, 3, 260, 1000)[i % 6] for i in range(len(new))], new, G * Hkv, Hkv, D, 16, seed=G)
     check(b, run(b, window, sinks), window, sinks)
 

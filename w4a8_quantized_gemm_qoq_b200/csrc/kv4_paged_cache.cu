@@ -9,13 +9,14 @@
 // the contiguous cache's write.
 //
 // Both kernels move 2 D + D/2 + 4 bytes per vector and are bound by HBM when
-// there are many vectors: FIGURES.
-// D / 8 lanes own a vector (16 bytes of FP16 and 4 bytes of codes each), so a warp
-// moves two vectors of 128 or four of 64 with full-width accesses. Where there
-// are enough vectors to fill the GPU all the same, a thread takes four, whose
-// loads are in flight together (one each: FIGURES1).
+// there are many vectors, by a launch's latency where there are few. D / 8 lanes
+// own a vector (16 bytes of FP16 and 4 bytes of codes each), so a warp moves
+// two vectors of 128 or four of 64 with full-width accesses. Measured, a write and a
+// read of 8192 tokens with 8 heads of 128 (85 MB): 25 us, 3.4 TB/s, the write
+// 15 of them; of 64 tokens 3.6 us.
 //
-// Issue slots bound them next, so operations per element are few:
+// The write's issue slots (157 instructions per 16-byte load, four fifths of the
+// slots taken) bound it before HBM does, so operations per element are few:
 //  - the extremes are found in FP16 pairs, then reduced over the lanes as (-lo, hi) pairs;
 //  - the quotients x / s come from the correctly rounded reciprocal and one
 //    residual FMA pair (Markstein's correction, as in the fused producers:
@@ -194,10 +195,12 @@ cudaError_t launch(const PagedCacheParams &p, bool write, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Four vectors per thread where that still makes a CTA for every SM.
+// Four vectors per thread, whose loads are in flight together, where that still
+// makes three CTAs for every SM (8 heads of 128, write and read: 1200 tokens 8.2 us,
+// one vector each 7.1; 2400 tokens 10.7 and 11.4; 8192 tokens 25.5 and 28.6).
 template <int D>
 cudaError_t launch(const PagedCacheParams &p, bool write, cudaStream_t stream) {
-    return p.N * p.Hkv * 2 * (D / 8) >= (int64_t)4 * kPcThreads * 148 ? launch<D, 4>(p, write, stream)
+    return p.N * p.Hkv * 2 * (D / 8) >= (int64_t)4 * kPcThreads * 3 * 148 ? launch<D, 4>(p, write, stream)
                                                                       : launch<D, 1>(p, write, stream);
 }
 

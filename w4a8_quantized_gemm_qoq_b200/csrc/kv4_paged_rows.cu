@@ -1,26 +1,31 @@
 // Paged KV4 attention for requests with few rows: n new tokens x G query
-// heads per KV head <= 32 (decode steps, short drafts).
+// heads per KV head <= 48 (decode steps, short drafts).
 //
 // The work is one pass over the request's K and V codes (D + 8 bytes per
 // token and KV head), so it is bound by HBM where sequences are long, and by
 // a launch's latency where they are short. Eight of a KV head's n x G (row,
 // head) pairs are the columns of the tensor-core products, so K and V are read
-// once for all of them; more pairs are columns of further pieces, which read
-// the same cache again (from L2, as they run side by side). That costs 8
-// columns x 64 tokens about 410 cycles of an SM; the many-rows kernel costs up to
-// 128 pairs x 128 tokens about 5000, so up to 32 pairs come here (32 sequences
-// x 5 rows x 4 heads: FIG us here, 127 there).
+// once for all of them; more pairs are the columns of further items, which read
+// the same cache again (from L2, as they run side by side).
 //
-// Pieces. The lengths are known on the device only, so every CTA works out the
-// same division: a request's visible tokens are 64-token tiles (those of the
-// sinks, then those of the window), four tiles are a round, and each (request,
-// KV head) is cut into ceil(rounds / S) even pieces, S the least of a few
-// candidates that gives at most one piece per resident CTA (four per SM), so
-// that all SMs end together whatever the mix of lengths. Pieces of one
-// (request, KV head) leave FP32 partial sums, which the last to arrive
-// combines in a fixed order.
+// Measured (8 KV heads of 128, 4 query heads each, GPU time of a call): 64
+// sequences of 1024 tokens in 23.5 us (3.1 TB/s), of 4096 in 68 us (4.2 TB/s),
+// 74 of 4096, which fill the GPU evenly, in 73 us (4.5 TB/s of 6.6 that a copy
+// reaches); one of 64 tokens in 6.5 us. At length a round (64 tokens in
+// each of 16 warps per SM) takes 4 us for some 15000 issued instructions: two
+// per cycle, the ALU pipe 55% busy with unpacking, so that neither bytes nor
+// one pipe but the mix of issue slots and latencies of 16 warps bounds it.
 //
-// Within a piece, each warp walks every fourth tile. Its K and V code tiles
+// The division. The lengths are known on the device only, so every CTA works out
+// the same division: a request's visible tokens are 64-token tiles (those of
+// the sinks, then those of the window), four tiles are a round, and the rounds of
+// all items, one after another, are cut into equal shares, one per resident CTA
+// (four per SM), so that all SMs end together whatever the mix of lengths (24
+// sequences of 100 to 32700 tokens: 49 us; cut into pieces of whole items
+// instead 56). An item that several CTAs share leaves FP32 partial sums,
+// which the last to arrive combines in a fixed order.
+//
+// Within a share, each warp walks every fourth tile. Its K and V code tiles
 // pass through a ring of three buffers (16-byte asynchronous copies, one
 // group per tile and tensor, so that two are in flight while one is computed); scales
 // and zeros are loaded one tile ahead, page numbers two. The copies go through
@@ -61,13 +66,15 @@ constexpr int kRwWarps = 4;
 constexpr int kRwThreads = 32 * kRwWarps;
 constexpr int kRwTile = 64;                   // tokens per warp tile
 constexpr int kRwResident = 4 * 148;          // CTAs that run at once
-constexpr int kRwStart = 2;                   // rounds that fit in the time in which an item starts and is merged
-constexpr int kRwWarpBatch = 128;             // requests whose division each warp works out itself
+constexpr int kRwStart = 2;                   // rounds that fit in the time in which an item starts and is merged (64
+                                              // sequences of 100 to 9000 tokens: 53, 48, 47, 50 us with 0, 1, 2, 3)
+constexpr int kRwWarpBatch = 128;             // requests whose division each warp works out itself (64 requests, 64 tokens
+                                              // each: 8.4 us, with the division kernel 12.8)
 constexpr float kRwSlack = 6.0f;              // log2 by which scores may exceed the running maximum
 
 struct RowsParams {
     PagedAttnParams a;
-    int g_inv;               // ceil(2^16 / G): c / G = c g_inv >> 16 for c < 32
+    int g_inv;               // ceil(2^16 / G): c / G = c g_inv >> 16 for c < 64
     int32_t *counters;       // [kRwResident], zero between calls
     float *part;             // [2 kRwResident][kRowsCols * D + 2 * kRowsCols]
     const int64_t *first;    // [B + 2] from the division kernel where B > kRwWarpBatch, else null
@@ -341,8 +348,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
     // In small pages eight lanes copy the codes of 16 tokens, which lie in one
     // page whatever its size: lane l the 16-byte chunks l % 8 + 8 i of the
     // tile's tokens 16 (l / 8) .. + 15. Else a lane copies chunks l + 32 i:
-    // 512 bytes in a row per copy (the former costs 3% there, and saves 7% where
-    // four lookups and addresses per tile and lane are the alternative).
+    // 512 bytes in a row per copy (the former would cost 3% there; it saves 5%
+    // where four lookups and addresses per tile and lane are the alternative).
     // Values are stored with a token's chunks permuted, so that the transposed
     // loads of 8 tokens' same chunk touch every bank once: chunk c of token t is
     // at c ^ (t / (8 / CPT)) % CPT, which is c ^ i % CPT in small pages and the same for every i else.

@@ -187,7 +187,7 @@ struct PagedAttnParams {
     int B, max_pages, max_new, Hq, Hkv, G, n_pages, page_shift, window, sinks;
     float qscale;        // log2(e) / sqrt(D)
 };
-constexpr int kRowsMax = 32;   // most (row, head) pairs per KV head of the few-rows kernel
+constexpr int kRowsMax = 48;   // most (row, head) pairs per KV head of the few-rows kernel
 constexpr int kRowsCols = 8;   // of which one piece takes so many, the columns of its products
 size_t rows_workspace_bytes(int64_t B, int64_t D);
 cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cudaStream_t stream);
