@@ -351,9 +351,20 @@ def kv4_decode_attention(q, kcache, vcache, seq_lens=None, ws=None, out=None, st
 #
 # A serving step makes these calls for every layer, so their checks are kept
 # short: one test of what a correct argument has, and the reason only where it
-# fails; pointers of the buffers that an object owns are kept with it.
+# fails; pointers of the buffers that an object owns are kept with it, and what
+# is needed of torch in names of this module from the first object on.
 
 _vp, _i64 = ctypes.c_void_p, ctypes.c_int64
+_Tensor = _int32 = _float16 = _empty = _get_device = _current_stream = None
+
+
+def _bind_torch():
+    global _Tensor, _int32, _float16, _empty, _get_device, _current_stream
+    if _Tensor is None:
+        import torch
+        _int32, _float16, _empty = torch.int32, torch.float16, torch.empty
+        _get_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _Tensor = torch.Tensor
 
 
 def _device_scope(device):
@@ -362,15 +373,9 @@ def _device_scope(device):
     return torch.cuda.device(device)
 
 
-def _current(index):
-    import torch
-    return torch._C._cuda_getDevice() == index
-
-
 def _raw_stream(stream, index):
     """The stream to launch on: the given one, or the device's current one."""
-    import torch
-    return _vp(torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    return _vp(_current_stream(index) if stream is None else stream.cuda_stream)
 
 
 def _stream_scope(stream):
@@ -380,19 +385,17 @@ def _stream_scope(stream):
 
 
 def _empty_fp16(shape, device, stream):
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=torch.float16, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=torch.float16, device=device)
+        return _empty(shape, dtype=_float16, device=device)
+    with _stream_scope(stream):
+        return _empty(shape, dtype=_float16, device=device)
 
 
 def _i32(t, shape, device, name):
     """Pointer of an int32 CUDA tensor of this shape on this device."""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and t.device == device and
+    if not (isinstance(t, _Tensor) and t.dtype is _int32 and t.shape == shape and t.device == device and
             t.is_contiguous()):
-        _cuda_tensor(t, torch.int32, name)
+        _cuda_tensor(t, _int32, name)
         if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
@@ -400,22 +403,23 @@ def _i32(t, shape, device, name):
 
 
 def _rows(t, heads, D, device, name):
-    """Pointer and row stride (in elements) of FP16 [N][heads][D] with dense heads
-    and any row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """Pointer, row stride (in elements) and rows of FP16 [N][heads][D] with
+    dense heads and any row stride; heads None: any number of them."""
+    if isinstance(t, _Tensor) and t.dtype is _float16 and t.device == device and t.dim() == 3:
+        n, h, d = t.shape
+        if d == D and (heads is None or h == heads):
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and (s1 == D or h == 1) or n == 0:
+                return _vp(t.data_ptr()), s0 if n > 1 else h * D, n
+            raise ValueError("the heads of a row of %s must be dense" % name)
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not torch.float16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.float16, t.dtype))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError("%s must have shape [N][%d][%d], got %s" % (name, heads, D, tuple(t.shape)))
+    if t.dtype is not _float16:
+        raise TypeError("%s must be %s, got %s" % (name, _float16, t.dtype))
     if t.device != device:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    n = t.shape[0]
-    s = t.stride()
-    if n and (s[2] != 1 or (heads > 1 and s[1] != D)):
-        raise ValueError("the heads of a row of %s must be dense" % name)
-    return _vp(t.data_ptr()), s[0] if n > 1 else heads * D
+    raise ValueError("%s must have shape [N][%s][%d], got %s" % (name, "heads" if heads is None else heads, D,
+                                                                  tuple(t.shape)))
 
 
 class PagedStep:
@@ -426,6 +430,7 @@ class PagedStep:
 
     def __init__(self, B, max_tokens, device="cuda"):
         import torch
+        _bind_torch()
         self._q_start = torch.zeros((B + 1,), dtype=torch.int32, device=device)
         self._positions = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
         self._slots = torch.full((max_tokens,), -1, dtype=torch.int32, device=device)
@@ -457,6 +462,7 @@ class PageTable:
 
     def _set(self, seq_lens, block_table, free_pages, free_count, page_size):
         import torch
+        _bind_torch()
         _cuda_tensor(seq_lens, torch.int32, "seq_lens")
         if seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
             raise ValueError("seq_lens [B], block_table [B][max_pages] and free_pages [n_pages] are expected")
@@ -483,7 +489,7 @@ class PageTable:
         are updated in place, unless kv_lens [B] and free_left [1] are given
         to take the new ones. Returns `step`."""
         device = self.device
-        if not _current(device.index):
+        if _get_device() != device.index:
             with _device_scope(device):
                 return self.assign(new_lens, step, kv_lens, free_left, stream)
         B, page_size, n_pages, max_pages = self._sizes
@@ -505,7 +511,7 @@ class PageTable:
         """End the requests b with leave[b] != 0 (int32 [B]): their pages are
         free again, their lengths 0."""
         device = self.device
-        if not _current(device.index):
+        if _get_device() != device.index:
             with _device_scope(device):
                 return self.release(leave, stream)
         B, page_size, n_pages, max_pages = self._sizes
@@ -543,6 +549,7 @@ class PagedKV4Cache:
 
     def _set(self, k_codes, k_params, v_codes, v_params):
         import torch
+        _bind_torch()
         for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
             _cuda_tensor(t, torch.uint8, name)
         for t, name in ((k_params, "k_params"), (v_params, "v_params")):
@@ -568,14 +575,13 @@ class PagedKV4Cache:
         """Quantise rows k, v [N][Hkv][D] FP16 (any row stride) into
         slots [N] int32; rows with a slot outside the cache are skipped."""
         device = self.device
-        if not _current(device.index):
+        if _get_device() != device.index:
             with _device_scope(device):
                 return self.write(k, v, slots, stream)
-        kp, ks = _rows(k, self.Hkv, self.D, device, "k")
-        vp, vs = _rows(v, self.Hkv, self.D, device, "v")
-        N = k.shape[0]
-        if v.shape[0] != N:
-            raise ValueError("k has %d rows, v %d" % (N, v.shape[0]))
+        kp, ks, N = _rows(k, self.Hkv, self.D, device, "k")
+        vp, vs, n = _rows(v, self.Hkv, self.D, device, "v")
+        if n != N:
+            raise ValueError("k has %d rows, v %d" % (N, n))
         code = lib().qoq_kv4_paged_write(kp, ks, vp, vs, _i32(slots, (N,), device, "slots"), N, *self._sizes,
                                          *self._ptrs, _raw_stream(stream, device.index))
         if code:
@@ -585,9 +591,8 @@ class PagedKV4Cache:
     def read(self, slots, k=None, v=None, stream=None):
         """The cached K and V of slots [N] as FP16 [N][Hkv][D] each (a sequence
         moved elsewhere, or handed to a dense kernel); 0 outside the cache."""
-        import torch
         device = self.device
-        if not _current(device.index):
+        if _get_device() != device.index:
             with _device_scope(device):
                 return self.read(slots, k, v, stream)
         N = slots.shape[0]
@@ -595,7 +600,7 @@ class PagedKV4Cache:
         shape = (N, self.Hkv, self.D)
         for t, name in ((k, "k"), (v, "v")):
             if t is not None:
-                _cuda_tensor(t, torch.float16, name)
+                _cuda_tensor(t, _float16, name)
                 if t.shape != shape or t.device != device:
                     raise ValueError("%s must have shape %s on %s" % (name, shape, device))
         k = _empty_fp16(shape, device, stream) if k is None else k
@@ -622,22 +627,21 @@ def kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window
     block_table [B][max_pages] holds of it, causally, and with window > 0 only
     to the latest `window` of them and the first `sinks`. max_new bounds the
     rows per request (1 for a decode step). Returns out [N][Hq][D] FP16."""
-    import torch
     device = cache.device
-    if not _current(device.index):
+    if _get_device() != device.index:
         with _device_scope(device):
             return kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window, sinks, ws, out, stream)
     Hkv, D, n_pages, page_size = cache._sizes
-    N, Hq = q.shape[0], q.shape[1]
-    qp, qs = _rows(q, Hq, cache.D, device, "q")
+    qp, qs, N = _rows(q, None, cache.D, device, "q")
+    Hq = q.shape[1]
     B, max_pages = block_table.shape
     if ws is None:
         with _stream_scope(stream):
             ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, cache.D, max_new), device)
     if out is None:
         out = _empty_fp16((N, Hq, cache.D), device, stream)
-    op, os_ = _rows(out, Hq, cache.D, device, "out")
-    if out.shape[0] != N or ws.buf.device != device:
+    op, os_, n = _rows(out, Hq, cache.D, device, "out")
+    if n != N or ws.buf.device != device:
         raise ValueError("out must have q's shape, and the workspace its device")
     n = ctypes.c_size_t(ws.buf.numel())
     code = lib().qoq_kv4_paged_attention(
