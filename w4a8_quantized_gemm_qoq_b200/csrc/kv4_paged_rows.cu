@@ -21,8 +21,8 @@
 // the sinks, then those of the window), four tiles are a round, and the rounds of
 // all items, one after another, are cut into equal shares, one per resident CTA
 // (four per SM), so that all SMs end together whatever the mix of lengths (24
-// sequences of 100 to 32700 tokens: 49 us; cut into pieces of whole items
-// instead 56). An item that several CTAs share leaves FP32 partial sums,
+// sequences of 100 to 32700 tokens in pages of 16: 46 us; cut into pieces of items
+// instead, before the lookups were spread over lanes, 56 against 52). An item that several CTAs share leaves FP32 partial sums,
 // which the last to arrive combines in a fixed order.
 //
 // Within a share, each warp walks every fourth tile. Its K and V code tiles
@@ -407,20 +407,18 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         auto tile_t0 = [&](int k) {
             return (k < tl.sink_tiles ? k : tl.first + (k - tl.sink_tiles)) * kRwTile;
         };
-        // The page of the lane's tokens of tile k: its number, or -1 past the
-        // sequence's end and for numbers outside the cache.
+        // The page of the lane's tokens of tile k, as the table has it (-1 past the
+        // sequence's end). It is looked at a tile later, when it has arrived:
+        // `checked` makes -1 of a number outside the cache and names the request.
         const int32_t *table = p.block_table + (int64_t)b * p.max_pages;
         auto load_page = [&](int k) {
             const int t = tile_t0(k) + part;
-            int pg = -1;
-            if (k < k_end && t < r.kv) {
-                pg = __ldg(table + (t >> p.page_shift));
-                if ((uint32_t)pg >= (uint32_t)p.n_pages) {
-                    paged_bad_request(p, b);
-                    pg = -1;
-                }
-            }
-            return pg;
+            return k < k_end && t < r.kv ? __ldg(table + (t >> p.page_shift)) : -1;
+        };
+        auto checked = [&](int k, int pg) {
+            if ((uint32_t)pg < (uint32_t)p.n_pages) return pg;
+            if (k < k_end && tile_t0(k) + part < r.kv) paged_bad_request(p, b);
+            return -1;
         };
         // Tile k's codes into the ring at `dst` as one copy group (empty past
         // the last tile). Tokens without a page copy page 0's codes, which
@@ -466,8 +464,10 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         int pgn;
         uint32_t kw[2] = {0u, 0u}, vw[2] = {0u, 0u};
         {
-            const int pg = load_page(k);
+            int pg = load_page(k);
             pgn = load_page(k + kRwWarps);
+            pg = checked(k, pg);
+            pgn = checked(k + kRwWarps, pgn);
             issue(k, false, pg, s0);
             issue(k, true, pg, s1);
             if (k < k_end) load_sz(k, pg, kw, vw);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
 
         for (; k < k_end; k += kRwWarps) {
             const int t0 = tile_t0(k);
-            const int pgnn = load_page(k + 2 * kRwWarps);
+            int pgnn = load_page(k + 2 * kRwWarps);
             uint32_t kwn[2] = {0u, 0u}, vwn[2] = {0u, 0u};
             if (k + kRwWarps < k_end) load_sz(k + kRwWarps, pgn, kwn, vwn);   // in flight while this tile is computed
             // Whether every column sees every token of the tile.
@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                 mma_16816(oz, az, pb0, pb1);
             }
             __syncwarp();   // every lane is done with the values: the keys after the next take their place
+            pgnn = checked(k + 2 * kRwWarps, pgnn);
             issue(k + 2 * kRwWarps, false, pgnn, s1);
             const uint32_t s = s0;
             s0 = s2, s2 = s1, s1 = s;
