@@ -21,9 +21,10 @@
 // the sinks, then those of the window), four tiles are a round, and the rounds of
 // all items, one after another, are cut into equal shares, one per resident CTA
 // (four per SM), so that all SMs end together whatever the mix of lengths (24
-// sequences of 100 to 32700 tokens in pages of 16: 46 us; cut into pieces of items
-// instead, before the lookups were spread over lanes, 56 against 52). An item that several CTAs share leaves FP32 partial sums,
-// which the last to arrive combines in a fixed order.
+// sequences of 100 to 32700 tokens in pages of 16 took 52 us when this was
+// introduced, 56 in even pieces of each item; 46 now). An item that several
+// CTAs share leaves FP32 partial sums, which the last to arrive combines in a
+// fixed order.
 //
 // Within a share, each warp walks every fourth tile. Its K and V code tiles
 // pass through a ring of three buffers (16-byte asynchronous copies, one
