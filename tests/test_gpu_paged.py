@@ -342,6 +342,26 @@ def test_fewer_tokens_than_rows():
     assert (out[:4] == 0).all() and (out[6:76] == 0).all()
 
 
+@pytest.mark.parametrize("new", [1, 70])
+def test_lengths_are_clamped_to_the_buffers(new):
+    """Negative lengths count as 0, lengths beyond the table as its capacity;
+    row ranges that run backwards as empty, beyond q as its rows."""
+    b = Batch([200 - new, 256 - new, 100], [new] * 3, 8, 2, 128, 16, seed=24)
+    b.table[b.table < 0] = 0   # every entry of the table names some page
+    table = b.table[:, :16].copy()
+    lens = np.array([-5, 2 ** 31 - 1, 100 + new], np.int32)
+    starts = np.array([0, new, 2 * new, 2 ** 31 - 1], np.int32)
+    ws = workspace(b)
+    out = host(qoq.kv4_paged_attention(dev(b.q), b.cache(), dev(table), dev(starts), dev(lens), new, ws=ws))
+    assert ws.status() == 0 and (out[:new] == 0).all()
+    b.table, b.kv = table, np.array([0, 256, 100 + new], np.int32)
+    check(b, out)
+    out = torch().full(b.q.shape, 7.0, dtype=torch().float16, device="cuda")
+    back = np.array([2 * new, new, 0, -3], np.int32)
+    qoq.kv4_paged_attention(dev(b.q), b.cache(), dev(table), dev(back), dev(lens), new, ws=ws, out=out)
+    assert ws.status() == 0 and (host(out) == 7.0).all()
+
+
 @pytest.mark.parametrize("max_new", [1, 4])
 def test_more_rows_than_promised(max_new):
     """A request with more rows than max_new is refused: its rows stay, the

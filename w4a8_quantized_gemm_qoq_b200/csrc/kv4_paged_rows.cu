@@ -159,7 +159,7 @@ __device__ __forceinline__ void rows_begin(const PagedAttnParams &p, RowsWork &w
     w.remaining = (int)min((int64_t)w.S, total - x);
     w.done = 0;
     w.b = b;
-    w.item = (int)((uint64_t)in_request / (uint32_t)length);
+    w.item = (int)((uint64_t)in_request / (uint32_t)max(length, 1));
     w.offset = (int)(in_request - (int64_t)w.item * length);
 }
 
@@ -208,7 +208,7 @@ __device__ __forceinline__ bool rows_divide(const PagedAttnParams &p, RowsWork &
     const int owner = __ffs((int)__ballot_sync(0xffffffffu, upto > x)) - 1;
     int64_t rest = x - __shfl_sync(0xffffffffu, upto - sum, owner);
     int b = owner * per;
-    for (;; ++b) {
+    for (; b + 1 < p.B; ++b) {
         const int64_t n = (int64_t)rows_length(p, b, w.same) * rows_items(p, b);
         if (rest < n) break;
         rest -= n;
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         const PagedRequest r = paged_request(p, b);
         const RowsTiles tl = rows_tiles(p, r);
         const int rounds = max(1, (tl.count + kRwWarps - 1) / kRwWarps);
-        const int groups = (r.n * p.G + kRowsCols - 1) / kRowsCols;
-        const int h = work_s.item / groups, group = work_s.item - h * groups;
+        const int groups = max(1, (r.n * p.G + kRowsCols - 1) / kRowsCols);
+        const int h = min(work_s.item / groups, p.Hkv - 1), group = work_s.item - h * groups;
         const int length = work_s.same ? work_s.same : rounds + kRwStart;
         const int count = min(length - work_s.offset, work_s.remaining - work_s.done);   // of this segment
         const int round0 = max(work_s.offset - kRwStart, 0), round1 = min(work_s.offset + count - kRwStart, rounds);
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                 if (seg.last_item) {
                     wk.item = 0;
                     do ++wk.b;
-                    while (rows_rounds(p, wk.b) == 0);
+                    while (wk.b + 1 < p.B && rows_rounds(p, wk.b) == 0);
                 } else {
                     ++wk.item;
                 }

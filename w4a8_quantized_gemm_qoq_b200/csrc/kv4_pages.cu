@@ -70,6 +70,11 @@ __device__ __forceinline__ int owner_of(const int32_t *start, int B, int x) {
     return lo;
 }
 
+// A cluster barrier in two halves: no CTA's shared memory is written from another
+// before it runs and has initialised it.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Raise `err` (at offset of this CTA's own variable) in every CTA of the cluster.
 __device__ __forceinline__ void cluster_raise(int32_t *err, int code, int ctas) {
     const uint32_t a = smem_u32(err);
@@ -98,6 +103,7 @@ __global__ void __launch_bounds__(kPgThreads) kv4_assign_kernel(const __grid_con
     const int P = 1 << p.page_shift;
     if (tid == 0) bad_pages = 0, bad_request = INT32_MAX;
     __syncthreads();
+    if (ctas > 1) cluster_arrive();   // this CTA runs and may be told of bad pages: waited for before it is
 
     // 1. Every CTA: the rows and pages before each request.
     const int count = *p.free_count;
@@ -137,6 +143,7 @@ __global__ void __launch_bounds__(kPgThreads) kv4_assign_kernel(const __grid_con
     if (code == 0 && (request >= 0 || rows > p.max_tokens || pages > count)) code = QOQ_ERR_WORKSPACE;
 
     // 2. This CTA's share of the page numbers that the step reads.
+    if (ctas > 1) cluster_wait();
     if (code == 0) {
         bool bad = false;
         for (int b = rank * kPgThreads + tid; b < p.B; b += ctas * kPgThreads)
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kPgThreads) kv4_assign_kernel(const __grid_con
         if (bad) cluster_raise(&bad_pages, QOQ_ERR_INVALID_ARG, ctas);
     }
     __syncthreads();
-    cluster_sync_all();   // every CTA has read the state, and knows of every bad page
+    if (ctas > 1) cluster_sync_all();   // every CTA has read the state, and knows of every bad page
     if (code == 0) code = bad_pages;
 
     // 3. This CTA's share of the step.
@@ -216,6 +223,7 @@ __global__ void __launch_bounds__(kPgThreads) kv4_release_kernel(const __grid_co
     const int P = 1 << p.page_shift;
     if (tid == 0) bad_pages = 0, bad_request = INT32_MAX;
     __syncthreads();
+    if (ctas > 1) cluster_arrive();   // this CTA runs and may be told of bad pages: waited for before it is
     const int count = *p.free_count;
     int64_t pages = 0;
     int code = count < 0 || count > p.n_pages ? QOQ_ERR_INVALID_ARG : 0;
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(kPgThreads) kv4_release_kernel(const __grid_co
     const int request = bad_request == INT32_MAX ? -1 : bad_request;
     if (request >= 0) code = QOQ_ERR_INVALID_ARG;
     if (code == 0 && pages > p.n_pages - count) code = QOQ_ERR_WORKSPACE;
+    if (ctas > 1) cluster_wait();
     if (code == 0) {
         bool bad = false;
         for (int g = rank * kPgThreads + tid; g < (int)pages; g += ctas * kPgThreads) {
@@ -247,7 +256,7 @@ __global__ void __launch_bounds__(kPgThreads) kv4_release_kernel(const __grid_co
         if (bad) cluster_raise(&bad_pages, QOQ_ERR_INVALID_ARG, ctas);
     }
     __syncthreads();
-    cluster_sync_all();   // every CTA has read the lengths and the count, and knows of every bad page
+    if (ctas > 1) cluster_sync_all();   // every CTA has read the lengths and the count, and knows of every bad page
     if (code == 0) code = bad_pages;
     if (code) {
         if (rank == 0 && tid == 0) record(p.status, code, request, 0, pages);
