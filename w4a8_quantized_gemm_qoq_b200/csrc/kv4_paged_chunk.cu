@@ -722,9 +722,9 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
         out1_at += two & (steps > 0);
         __syncwarp();
     };
-    auto walk = [&](auto role) {
+    auto walk = [&](auto agree, auto role) {
         ChunkPiece *c = &piece_s[warp][0];
-        for (int round = 0; locate(round, c); ++round) {
+        for (int round = 0; agree(locate(round, c)); ++round) {
             role(*c);
             advance(*c);
         }
@@ -907,7 +907,9 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < CPL; ++i) part[i] = (tk + i * kStride) >> p.page_shift;
         const int part_t = t >> p.page_shift;   // of token t
-        walk([&](const ChunkPiece &pc) {
+        // The four warps meet in every step, so that they go on or stop (another
+        // role may just have given up) as one.
+        walk([](bool more) { return !named_bar_any(2, 128, !more); }, [&](const ChunkPiece &pc) {
             const int k0 = pc.k0, k1 = pc.k1, kv = pc.r.kv;
             if (k0 == k1) return;
             const int32_t *table = p.block_table + (int64_t)pc.b * p.max_pages;
@@ -1033,7 +1035,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
     } else {
         // ---------------------------------------------------------- issue
         regs_dec<kRegsIssue>();
-        if (warp == 12) walk([&](const ChunkPiece &c) {
+        if (warp == 12) walk([](bool more) { return more; }, [&](const ChunkPiece &c) {
             const int steps = c.k1 - c.k0;
             const bool two = c.rows > 128;
             constexpr uint32_t id_s = idesc_f16(128, kChKeys, false), id_o = idesc_f16(128, D, true);
