@@ -62,8 +62,8 @@ constexpr int kChThreads = 512;      // warpgroups: softmax 0 and 1, unpack, iss
 constexpr int kChSlots = 2 * kChCtas;   // pieces of divided items
 constexpr int kChOverhead = 3;       // cost of a piece beside its steps, in steps
 // Registers per thread: the pool is 512 threads x 128, of which the roles take
-// 256 x 184 + 128 x 104 + 128 x 40 = 65536.
-constexpr int kRegsSoftmax = 184, kRegsUnpack = 104, kRegsIssue = 40;
+// 256 x 176 + 128 x 104 + 128 x 56 = 65536.
+constexpr int kRegsSoftmax = 176, kRegsUnpack = 104, kRegsIssue = 56;
 constexpr float kChSlack = 6.0f;     // log2 by which scores may exceed the running maximum
 constexpr int kDvThreads = 1024;
 
