@@ -1040,8 +1040,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             const bool two = c.rows > 128;
             constexpr uint32_t id_s = idesc_f16(128, kChKeys, false), id_o = idesc_f16(128, D, true);
             if (lane == 0 && steps > 0) {
-                bool ok = wait_bounded(&bars.q[0], out_at & 1, wd, kSiteChunkQ, (int)piece_at) &&
-                          (!two || wait_bounded(&bars.q[1], out1_at & 1, wd, kSiteChunkQ, (int)piece_at));
+                bool ok = wait_bounded(&bars.q[0], out_at & 1, wd, kSiteChunkQ, (int)piece_at);
                 const uint32_t qd = desc_low(base + L::kQ, 16), kd = desc_low(base + L::kK, 16);
                 const uint32_t vd = desc_low(base + L::kV, L::kPanel);
                 auto scores = [&](int i, uint32_t stage) {
@@ -1063,7 +1062,11 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                     if (ok) {
                         tc_fence_after();
                         scores(0, s0 & 1);
-                        if (two) scores(1, s0 & 1);
+                        // The second tile's queries come later, by as much as its softmax was behind in the last piece.
+                        if (two && (ok = wait_bounded(&bars.q[1], out1_at & 1, wd, kSiteChunkQ, (int)piece_at))) {
+                            tc_fence_after();
+                            scores(1, s0 & 1);
+                        }
                         tc_commit(&bars.k_free[s0 & 1]);
                     }
                     for (int k = 0; ok && k < steps; ++k) {
