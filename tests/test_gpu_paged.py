@@ -222,6 +222,24 @@ def test_write_and_read_are_exact(N, Hkv, D, page):
                               want.view(np.uint16) & 0x7FFF | (want < 0) * 0x8000), "read"
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_written_bytes_of_not_finite_values(D):
+    """Infinities and NaN among the values: the contiguous cache's bytes."""
+    x = np.random.default_rng(D).standard_normal((16, 1, D)).astype(np.float16)
+    x[0, 0, 3], x[1, 0, 7], x[2, 0, 60], x[3, 0, :] = np.inf, -np.inf, np.nan, np.nan
+    x[4, 0, 1], x[4, 0, 2], x[5, 0, 5], x[5, 0, 6] = np.inf, -np.inf, np.nan, np.inf
+    a = qoq.KV4Cache(1, 1, 16, D).write(dev(x.reshape(1, 1, 16, D)))
+    c = qoq.PagedKV4Cache(1, 1, 16, D)
+    c.write(dev(x), dev(x), dev(np.arange(16, dtype=np.int32)))
+    for got in (c.k_codes, c.v_codes):
+        assert np.array_equal(host(got).reshape(16, D // 2), host(a.codes).reshape(16, D // 2))
+    for got in (c.k_params, c.v_params):
+        s, z = host(got).reshape(16, 2)[:, 0], host(got).reshape(16, 2)[:, 1]
+        assert np.array_equal(np.isnan(s), np.isnan(host(a.scales).reshape(16)))
+        assert np.array_equal(np.nan_to_num(s), np.nan_to_num(host(a.scales).reshape(16)))
+        assert np.array_equal(z.view(np.uint16), host(a.zeros).reshape(16).view(np.uint16))
+
+
 def test_paged_and_contiguous_caches_hold_the_same_bytes():
     _, K, _ = inputs.make_decode_attention(2, 48, 8, 4, 128, seed=5)
     a = qoq.KV4Cache(2, 4, 48, 128).write(dev(K))

@@ -9,14 +9,15 @@
 // the contiguous cache's write.
 //
 // Both kernels move 2 D + D/2 + 4 bytes per vector and are bound by HBM when
-// there are many vectors, by a launch's latency where there are few. D / 8 lanes
-// own a vector (16 bytes of FP16 and 4 bytes of codes each), so a warp moves
-// two vectors of 128 or four of 64 with full-width accesses. Measured, a write and a
-// read of 8192 tokens with 8 heads of 128 (85 MB): 25 us, 3.4 TB/s, the write
-// 15 of them; of 64 tokens 3.6 us.
+// there are many vectors, by a launch's latency where there are few. D / 16 lanes
+// own a vector, two chunks of 8 values each, so that a load or store of theirs is
+// 128 or 32 bytes in a row. Measured, a write and a read of 8192 tokens with 8
+// heads of 128 (85 MB): 22.6 us, 3.8 TB/s (with one chunk per lane 25); of 1200
+// tokens 5.6 us, of 64 tokens 3.7. Two vectors per thread take 5.9 us for 1200 tokens, 21.9
+// for 8192: not worth a second form.
 //
-// The write's issue slots (157 instructions per 16-byte load, four fifths of the
-// slots taken) bound it before HBM does, so operations per element are few:
+// With one chunk per lane four fifths of the write's issue slots were taken, so
+// operations per element are few:
 //  - the extremes are found in FP16 pairs, then reduced over the lanes as (-lo, hi) pairs;
 //  - the quotients x / s come from the correctly rounded reciprocal and one
 //    residual FMA pair (Markstein's correction, as in the fused producers:
@@ -37,7 +38,7 @@ namespace qoq {
 
 namespace {
 
-constexpr int kPcThreads = 256;
+constexpr int kPcThreads = 128;
 
 struct PagedCacheParams {
     const __half *k, *v;
@@ -60,14 +61,13 @@ __device__ __forceinline__ float quotient(float a, float b, float y) {
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 
-// A CTA takes one head of PER x VPC rows (so that the codes and parameters of
-// neighbouring tokens, neighbours in a page, are stored together), a thread of
-// the rows `row`, row + VPC, ...
-template <int VPC, int PER>
-__device__ __forceinline__ void vectors_of(const PagedCacheParams &p, int64_t &row, int &h) {
+// A CTA takes one head of kPcThreads / LPV rows, so that the codes and parameters
+// of neighbouring tokens, neighbours in a page, are stored together.
+template <int LPV>
+__device__ __forceinline__ void vector_of(const PagedCacheParams &p, int64_t &row, int &h) {
     const uint32_t block = blockIdx.x / (uint32_t)p.Hkv;
     h = (int)(blockIdx.x - block * (uint32_t)p.Hkv);
-    row = (int64_t)block * (PER * VPC) + threadIdx.x / (kPcThreads / VPC);
+    row = (int64_t)block * (kPcThreads / LPV) + threadIdx.x / LPV;
 }
 
 // The place of a slot's vector of head h in the cache, (page * Hkv + head) *
@@ -79,53 +79,48 @@ __device__ __forceinline__ int64_t place_of(const PagedCacheParams &p, int64_t r
     return (((int64_t)(slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
 }
 
-template <int D, int PER>
-__global__ void __launch_bounds__(kPcThreads) kv4_paged_write_kernel(const __grid_constant__ PagedCacheParams p) {
-    constexpr int LPV = D / 8, VPC = kPcThreads / LPV;   // lanes per vector, vectors per CTA and turn
+template <int D>
+__global__ void __launch_bounds__(kPcThreads, 16) kv4_paged_write_kernel(const __grid_constant__ PagedCacheParams p) {
+    constexpr int LPV = D / 16;   // lanes per vector
     const int l = threadIdx.x % LPV;
     const bool is_v = blockIdx.y != 0;
-    const int64_t stride = is_v ? p.v_stride : p.k_stride;
     int64_t row;
     int h;
-    vectors_of<VPC, PER>(p, row, h);
-    const uint4 *from = reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + row * stride + h * D) + l;
-    int64_t at[PER];
-    uint4 u[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        u[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row + i * VPC < p.N) u[i] = __ldg(from + i * (VPC * stride / 8));
-        at[i] = place_of(p, row + i * VPC, h);
+    vector_of<LPV>(p, row, h);
+    const uint4 *from = reinterpret_cast<const uint4 *>((is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride) + h * D) + l;
+    uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};   // chunks l and l + LPV of the vector
+    if (row < p.N) {
+        u[0] = __ldg(from);
+        u[1] = __ldg(from + LPV);
     }
-    __half2 mine;   // (-lo, hi) of the vector l % PER
+    const int64_t at = place_of(p, row, h);
+    // (-lo, hi) of the lane's 16 values, then of the vector's lanes; a NaN counts for neither.
+    __half2 mn[2], mx[2];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const __half2 a = as_half2(u[i].x), b = as_half2(u[i].y), c = as_half2(u[i].z), d = as_half2(u[i].w);
-        // Of the lane's 8 values, then of the vector's lanes; a NaN counts for neither.
-        const __half2 nm = __hneg2(__hmin2(__hmin2(a, b), __hmin2(c, d))), mx = __hmax2(__hmax2(a, b), __hmax2(c, d));
-        __half2 ext = __hmax2(__hmax2(__lows2half2(nm, mx), __highs2half2(nm, mx)), __floats2half2_rn(0.0f, 0.0f));
-#pragma unroll
-        for (int o = LPV / 2; o > 0; o >>= 1)   // the whole warp takes part
-            ext = __hmax2(ext, as_half2(__shfl_xor_sync(0xffffffffu, half2_bits(ext), o)));
-        if (i == 0 || l % PER == i) mine = ext;
+    for (int c = 0; c < 2; ++c) {
+        const __half2 x = as_half2(u[c].x), y = as_half2(u[c].y), z = as_half2(u[c].z), w = as_half2(u[c].w);
+        mn[c] = __hmin2(__hmin2(x, y), __hmin2(z, w));
+        mx[c] = __hmax2(__hmax2(x, y), __hmax2(z, w));
     }
-    // A lane works out one vector's scale, its reciprocal and the zero.
-    const float neg_lo = __low2float(mine);
-    const __half sh = __float2half_rn(__fdiv_rn(__fadd_rn(__high2float(mine), neg_lo), 15.0f));
-    const float scale = __half2float(sh), rcp = __frcp_rn(scale);
-    const __half zh = __int2half_rn(scale != 0.0f ? (int)rintf(quotient(neg_lo, scale, rcp)) : 0);
-    const uint32_t param = half2_bits(__halves2half2(sh, zh));
+    const __half2 nm = __hneg2(__hmin2(mn[0], mn[1])), m = __hmax2(mx[0], mx[1]);
+    __half2 ext = __hmax2(__hmax2(__lows2half2(nm, m), __highs2half2(nm, m)), __floats2half2_rn(0.0f, 0.0f));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const uint32_t sz = __shfl_sync(0xffffffffu, param, i, LPV);
-        const float y = __shfl_sync(0xffffffffu, rcp, i, LPV);
-        if (at[i] < 0) continue;
-        const float s = half_lo(sz), zf = __half2float(half_hi(sz));
-        uint32_t codes = 0u;
-        if (s != 0.0f) {
-            const uint64_t y2 = pair_of(y, y), s2 = pair_of(-s, -s), z2 = pair_of(zf, zf);
-            const uint64_t round2 = pair_of(kRoundInt, kRoundInt);
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+    for (int o = LPV / 2; o > 0; o >>= 1)   // the whole warp takes part
+        ext = __hmax2(ext, as_half2(__shfl_xor_sync(0xffffffffu, half2_bits(ext), o)));
+    if (at < 0) return;
+    const float neg_lo = __low2float(ext);
+    const __half sh = __float2half_rn(__fdiv_rn(__fadd_rn(__high2float(ext), neg_lo), 15.0f));
+    const float s = __half2float(sh);
+    float zf = 0.0f;
+    uint32_t codes[2] = {0u, 0u};
+    if (s != 0.0f) {
+        const float y = __frcp_rn(s);
+        zf = rintf(quotient(neg_lo, s, y));
+        const uint64_t y2 = pair_of(y, y), s2 = pair_of(-s, -s), z2 = pair_of(zf, zf);
+        const uint64_t round2 = pair_of(kRoundInt, kRoundInt);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
             // A sum's bits are those of 1.5 * 2^23 plus the code: the former's share of the shifted sum goes last.
             uint32_t shares = 0u;
 #pragma unroll
@@ -133,75 +128,61 @@ __global__ void __launch_bounds__(kPcThreads) kv4_paged_write_kernel(const __gri
                 const float2 x = __half22float2(as_half2(w[e]));
                 const uint64_t x2 = pair_of(x.x, x.y), q = mul2(x2, y2);
                 const float2 r = of_pair(add2(add2(fma2(fma2(q, s2, x2), y2, q), round2), z2));   // Markstein's, as above
-                codes += __float_as_uint(fminf(fmaxf(r.x, kRoundInt), kRoundInt + 15.0f)) << (8 * e);   // NaN: 0
-                codes += __float_as_uint(fminf(fmaxf(r.y, kRoundInt), kRoundInt + 15.0f)) << (8 * e + 4);
+                codes[c] += __float_as_uint(fminf(fmaxf(r.x, kRoundInt), kRoundInt + 15.0f)) << (8 * e);   // NaN: 0
+                codes[c] += __float_as_uint(fminf(fmaxf(r.y, kRoundInt), kRoundInt + 15.0f)) << (8 * e + 4);
                 shares += 0x4B400000u * 17u << (8 * e);
             }
-            codes -= shares;
+            codes[c] -= shares;
         }
-        reinterpret_cast<uint32_t *>(is_v ? p.v_codes : p.k_codes)[at[i] * LPV + l] = codes;
-        if (l == i) (is_v ? p.v_params : p.k_params)[at[i]] = as_half2(sz);
     }
+    uint32_t *to = reinterpret_cast<uint32_t *>(is_v ? p.v_codes : p.k_codes) + at * (D / 8) + l;
+    to[0] = codes[0];
+    to[LPV] = codes[1];
+    if (l == 0) (is_v ? p.v_params : p.k_params)[at] = __halves2half2(sh, __int2half_rn((int)zf));
 }
 
-template <int D, int PER>
-__global__ void __launch_bounds__(kPcThreads) kv4_paged_read_kernel(const __grid_constant__ PagedCacheParams p) {
-    constexpr int LPV = D / 8, VPC = kPcThreads / LPV;
+template <int D>
+__global__ void __launch_bounds__(kPcThreads, 16) kv4_paged_read_kernel(const __grid_constant__ PagedCacheParams p) {
+    constexpr int LPV = D / 16;
     const int l = threadIdx.x % LPV;
     const bool is_v = blockIdx.y != 0;
-    const uint32_t *codes = reinterpret_cast<const uint32_t *>(is_v ? p.v_codes : p.k_codes) + l;
-    const uint32_t *params = reinterpret_cast<const uint32_t *>(is_v ? p.v_params : p.k_params);
     int64_t row;
     int h;
-    vectors_of<VPC, PER>(p, row, h);
-    uint4 *to = reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out) + (row * p.Hkv + h) * LPV + l;
-    int64_t at[PER];
-    uint32_t c[PER], sz[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) at[i] = place_of(p, row + i * VPC, h);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        c[i] = sz[i] = 0u;
-        if (at[i] >= 0) {
-            c[i] = __ldg(codes + at[i] * LPV);
-            sz[i] = __ldg(params + at[i]);
-        }
+    vector_of<LPV>(p, row, h);
+    if (row >= p.N) return;
+    const int64_t at = place_of(p, row, h);
+    uint32_t c[2] = {0u, 0u}, sz = 0u;
+    if (at >= 0) {
+        const uint32_t *codes = reinterpret_cast<const uint32_t *>(is_v ? p.v_codes : p.k_codes) + at * (D / 8) + l;
+        c[0] = __ldg(codes);
+        c[1] = __ldg(codes + LPV);
+        sz = __ldg(reinterpret_cast<const uint32_t *>(is_v ? p.v_params : p.k_params) + at);
     }
+    const __half2 s = __low2half2(as_half2(sz));
+    const __half2 z = __hadd2(__high2half2(as_half2(sz)), __floats2half2_rn(1024.0f, 1024.0f));
+    uint4 *to = reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out) + (row * p.Hkv + h) * (D / 8) + l;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (row + i * VPC >= p.N) break;
-        const __half2 s = __low2half2(as_half2(sz[i]));
-        const __half2 z = __hadd2(__high2half2(as_half2(sz[i])), __floats2half2_rn(1024.0f, 1024.0f));
+    for (int x = 0; x < 2; ++x) {
         uint32_t r[4];   // codes e and e + 4 in r[e]
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t q = (c[i] >> (4 * e) & 0x000F000Fu) | 0x64006400u;
+            const uint32_t q = (c[x] >> (4 * e) & 0x000F000Fu) | 0x64006400u;
             r[e] = half2_bits(__hmul2(__hsub2(as_half2(q), z), s));
         }
-        to[(int64_t)i * VPC * p.Hkv * LPV] =
-            make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
-                       __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
+        to[x * LPV] = make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                                 __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
     }
 }
 
-template <int D, int PER>
-cudaError_t launch(const PagedCacheParams &p, bool write, cudaStream_t stream) {
-    constexpr int rows = PER * kPcThreads / (D / 8);   // per CTA
-    const dim3 grid((unsigned)((p.N + rows - 1) / rows * p.Hkv), 2);
-    if (write)
-        kv4_paged_write_kernel<D, PER><<<grid, kPcThreads, 0, stream>>>(p);
-    else
-        kv4_paged_read_kernel<D, PER><<<grid, kPcThreads, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-// Four vectors per thread, whose loads are in flight together, where that still
-// makes three CTAs for every SM (8 heads of 128, write and read: 1200 tokens 8.2 us,
-// one vector each 7.1; 2400 tokens 10.7 and 11.4; 8192 tokens 25.5 and 28.6).
 template <int D>
 cudaError_t launch(const PagedCacheParams &p, bool write, cudaStream_t stream) {
-    return p.N * p.Hkv * 2 * (D / 8) >= (int64_t)4 * kPcThreads * 3 * 148 ? launch<D, 4>(p, write, stream)
-                                                                      : launch<D, 1>(p, write, stream);
+    constexpr int rows = kPcThreads / (D / 16);   // per CTA
+    const dim3 grid((unsigned)((p.N + rows - 1) / rows * p.Hkv), 2);
+    if (write)
+        kv4_paged_write_kernel<D><<<grid, kPcThreads, 0, stream>>>(p);
+    else
+        kv4_paged_read_kernel<D><<<grid, kPcThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
