@@ -200,8 +200,12 @@ __global__ void __launch_bounds__(kDvThreads) kv4_chunk_division_kernel(const __
         for (int c = 0; c < kCandidates; ++c) {
             const float all = warp_sum(lane < warps ? sums_s[2 * c][lane] : 0.0f);
             const float cut = warp_sum(lane < warps ? sums_s[2 * c + 1][lane] : 0.0f);
-            // A cut piece also writes its rows as FP32 and has them read again.
-            const float cost = ceilf(all / kChCtas) * (steps + all * (float)kChOverhead + cut) / all;
+            // A cut piece also writes its rows as FP32 and has them read again, by
+            // one more kernel: half a step on top of the estimate. Prompts of 300
+            // and 500 tokens take 25 and 30 us uncut, as they then are, and 31 and 39
+            // cut; with a whole step, 8 chunks of 200 to 500 tokens stay uncut
+            // too, 112 us and not 105.
+            const float cost = ceilf(all / kChCtas) * (steps + all * (float)kChOverhead + cut) / all + (cut > 0.0f ? 0.5f : 0.0f);
             if (cut <= (float)kChSlots && cost < best) best = cost, S = candidate(c);
         }
     }
