@@ -355,14 +355,14 @@ def kv4_decode_attention(q, kcache, vcache, seq_lens=None, ws=None, out=None, st
 # is needed of torch in names of this module from the first object on.
 
 _vp, _i64 = ctypes.c_void_p, ctypes.c_int64
-_Tensor = _int32 = _float16 = _empty = _get_device = _current_stream = None
+_Tensor = _int32 = _float16 = _empty_like = _get_device = _current_stream = None
 
 
 def _bind_torch():
-    global _Tensor, _int32, _float16, _empty, _get_device, _current_stream
+    global _Tensor, _int32, _float16, _empty_like, _get_device, _current_stream
     if _Tensor is None:
         import torch
-        _int32, _float16, _empty = torch.int32, torch.float16, torch.empty
+        _int32, _float16, _empty_like = torch.int32, torch.float16, torch.empty_like
         _get_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _Tensor = torch.Tensor
 
@@ -384,11 +384,12 @@ def _stream_scope(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _empty_fp16(shape, device, stream):
+def _empty_fp16(like, shape, stream):
+    """An FP16 tensor beside `like`, which is one too."""
     if stream is None:
-        return _empty(shape, dtype=_float16, device=device)
+        return like.new_empty(shape)
     with _stream_scope(stream):
-        return _empty(shape, dtype=_float16, device=device)
+        return like.new_empty(shape)
 
 
 def _i32(t, shape, device, name):
@@ -603,8 +604,9 @@ class PagedKV4Cache:
                 _cuda_tensor(t, _float16, name)
                 if t.shape != shape or t.device != device:
                     raise ValueError("%s must have shape %s on %s" % (name, shape, device))
-        k = _empty_fp16(shape, device, stream) if k is None else k
-        v = _empty_fp16(shape, device, stream) if v is None else v
+        k = _empty_fp16(self._tensors[1], shape, stream) if k is None else k
+        if v is None:
+            v = _empty_like(k) if stream is None else _empty_fp16(k, shape, stream)
         code = lib().qoq_kv4_paged_read(sp, N, *self._sizes, *self._ptrs, _vp(k.data_ptr()), _vp(v.data_ptr()),
                                         _raw_stream(stream, device.index))
         if code:
@@ -639,7 +641,7 @@ def kv4_paged_attention(q, cache, block_table, q_start, kv_lens, max_new, window
         with _stream_scope(stream):
             ws = Workspace(kv4_paged_workspace_bytes(B, N, Hq, cache.Hkv, cache.D, max_new), device)
     if out is None:
-        out = _empty_fp16((N, Hq, cache.D), device, stream)
+        out = _empty_fp16(q, (N, Hq, cache.D), stream)
     op, os_, n = _rows(out, Hq, cache.D, device, "out")
     if n != N or ws.buf.device != device:
         raise ValueError("out must have q's shape, and the workspace its device")
