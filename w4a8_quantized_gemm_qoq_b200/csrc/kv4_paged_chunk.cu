@@ -5,7 +5,7 @@
 // (row, head) pairs of one request and KV head, as two tiles of 128 rows, and
 // walks the request's visible keys 128 at a time:
 //   S = Q . C_K^T      tcgen05.mma, both operands in shared memory, FP32 in TMEM
-//   x = S s_K c, online softmax in FP32 (one thread per row), P = p s_V as FP16
+//   x = S s_K c, online softmax in FP32 (a warp per 32 rows), P = p s_V as FP16
 //   O += P . C_V       tcgen05.mma, P in TMEM, FP32 accumulator in TMEM
 // C = q - z are the zero-subtracted codes, small integers that FP16 holds
 // exactly, so the only rounding before the output is that of P. Scales are per
