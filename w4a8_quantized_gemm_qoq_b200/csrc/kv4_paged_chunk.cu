@@ -611,7 +611,9 @@ __device__ __forceinline__ void softmax_rows(uint32_t ts, uint32_t kf, uint32_t 
                     b.x[i >> 1][2 * j + (i & 1)] = add2(b.x[i >> 1][2 * j + (i & 1)], pair_of(-up, -up));
             }
             __syncwarp();
-            // The step's weights stored so far.
+            // The step's weights stored so far. A load of tensor memory is ordered
+            // behind this warp's own stores of it by their wait alone.
+            if (q > 0) tmem_st_wait();
 #pragma unroll 1
             for (int o = 0; o < q; ++o)
 #pragma unroll
