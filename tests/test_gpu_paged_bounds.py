@@ -1,11 +1,14 @@
-"""Paged KV4 attention on the GPU at the borders of its stated bound (the bar
-of paged_case.py): inputs for which one rounding, one hidden token or one wait
-too few would show."""
+"""The paged KV4 calls on the GPU where little separates a right answer from a
+wrong one: attention at the borders of its stated bound (the bar of
+paged_case.py), and calls beside one another."""
+import threading
+
 import numpy as np
 import pytest
 
-from gpu_helpers import torch
+from gpu_helpers import host, torch
 from paged_case import Batch, check, run
+from w4a8_quantized_gemm_qoq_b200 import qoq
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
 
@@ -45,3 +48,49 @@ def test_a_maximum_that_rises_in_every_block(D, rise, window, sinks):
         level = (t // 32) * rise * np.log(2.0) / np.sqrt(D)
         put(b, r, t, np.broadcast_to(level[:, None, None], (len(t), 2, D)).copy(), "k")
     check(b, run(b, window, sinks), window, sinks)
+
+
+def test_page_steps_of_several_threads():
+    """Host threads with tables of different sizes above 4096 requests, each on
+    its own stream: no step is refused for what another thread's needs."""
+    t = torch()
+    go, failed = threading.Barrier(3), []
+
+    def serve(B):
+        try:
+            s = t.cuda.Stream()
+            pt, step = qoq.PageTable(B, 8, B, 16), qoq.PagedStep(B, 0)
+            none, leave = (t.zeros(B, dtype=t.int32, device="cuda") for _ in range(2))
+            t.cuda.synchronize()
+            go.wait()
+            for _ in range(6000):
+                pt.assign(none, step, stream=s)
+                pt.release(leave, stream=s)
+            s.synchronize()
+            assert pt.status() == 0
+        except Exception as e:
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=serve, args=(B,)) for B in (16384, 4200, 12500)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not failed, failed
+
+
+def test_a_captured_page_step_beside_a_smaller_one():
+    """A step of 16384 requests, captured before and replayed after one of 4200."""
+    t = torch()
+    B = 16384
+    pt, step, n = qoq.PageTable(B, 2, B, 16), qoq.PagedStep(B, B), t.ones(B, dtype=t.int32, device="cuda")
+    small, small_step = qoq.PageTable(4200, 2, 4200, 16), qoq.PagedStep(4200, 4200)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        pt.assign(n, step)
+    small.assign(n[:4200], small_step)
+    g.replay()
+    small.assign(n[:4200], small_step)
+    g.replay()
+    assert pt.status() == 0 and small.status() == 0
+    assert (host(pt.seq_lens) == 2).all() and (host(small.seq_lens) == 2).all()

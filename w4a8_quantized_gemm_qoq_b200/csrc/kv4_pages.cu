@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kv4_paged.cuh"
 #include "qoq_device.cuh"
 #include "qoq_internal.h"
 
@@ -277,10 +278,15 @@ __global__ void __launch_bounds__(kPgThreads) kv4_release_kernel(const __grid_co
 // eight (the portable size).
 int page_ctas(int64_t B, int64_t work) { return B <= 1024 && work <= 4 * kPgThreads ? 1 : 8; }
 
+// The kernel's shared-memory limit belongs to the process and not to a call:
+// it is set once, to what the largest batch needs, since a call that set its
+// own need would lower the limit between another thread's setting and launch.
 template <typename Params>
-cudaError_t launch_cluster(void (*kernel)(Params), const Params &p, int ctas, size_t smem, cudaStream_t stream) {
+cudaError_t launch_cluster(void (*kernel)(Params), SmemOptIn &opt_in, int words, const Params &p, int ctas,
+                           cudaStream_t stream) {
+    const size_t per = sizeof(int32_t) * (size_t)words, smem = per * (size_t)p.B;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = opt_in.set(kernel, (int)(per * kMaxPagedBatch));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -322,7 +328,8 @@ cudaError_t launch_pages_assign(const int32_t *seq_lens, const int32_t *new_lens
     p.max_pages = (int)max_pages;
     p.max_tokens = (int)max_tokens;
     p.page_shift = page_shift;
-    return launch_cluster(kv4_assign_kernel, p, page_ctas(B, max_tokens), 3 * sizeof(int32_t) * (size_t)B, stream);
+    static SmemOptIn opt_in;
+    return launch_cluster(kv4_assign_kernel, opt_in, 3, p, page_ctas(B, max_tokens), stream);
 }
 
 cudaError_t launch_pages_release(const int32_t *leave, int64_t B, int page_shift, int32_t *seq_lens,
@@ -339,7 +346,8 @@ cudaError_t launch_pages_release(const int32_t *leave, int64_t B, int page_shift
     p.n_pages = (int)n_pages;
     p.max_pages = (int)max_pages;
     p.page_shift = page_shift;
-    return launch_cluster(kv4_release_kernel, p, page_ctas(B, n_pages), sizeof(int32_t) * (size_t)B, stream);
+    static SmemOptIn opt_in;
+    return launch_cluster(kv4_release_kernel, opt_in, 1, p, page_ctas(B, n_pages), stream);
 }
 
 }  // namespace qoq
