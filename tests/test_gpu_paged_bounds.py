@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 from gpu_helpers import host, torch
+from oracle import kv4_paged
 from paged_case import Batch, check, run
 from w4a8_quantized_gemm_qoq_b200 import qoq
 
@@ -94,3 +95,19 @@ def test_a_captured_page_step_beside_a_smaller_one():
     g.replay()
     assert pt.status() == 0 and small.status() == 0
     assert (host(pt.seq_lens) == 2).all() and (host(small.seq_lens) == 2).all()
+
+
+@pytest.mark.parametrize("B", [4050, 4080, 4096, 4097, 12200, 12288, 12289, 16384])
+def test_page_steps_of_many_requests(B):
+    """Batches around those at which a step's shared memory passes what a kernel
+    gets without asking: a step in which every request begins, and its release."""
+    t = torch()
+    pt, step, n = qoq.PageTable(B, 2, B, 16), qoq.PagedStep(B, B), t.ones(B, dtype=t.int32, device="cuda")
+    free = host(pt.free_pages)
+    pt.assign(n, step)
+    want = kv4_paged.assign(np.zeros(B, int), np.ones(B, int), free, B, np.full((B, 2), -1), 16, B)
+    for name in ("q_start", "positions", "slots"):
+        assert np.array_equal(host(getattr(step, name)), want[name]), name
+    assert np.array_equal(host(pt.block_table), want["block_table"]) and int(host(pt.free_count)[0]) == 0
+    pt.release(n)
+    assert np.array_equal(host(pt.free_pages), free) and not host(pt.seq_lens).any() and pt.status() == 0

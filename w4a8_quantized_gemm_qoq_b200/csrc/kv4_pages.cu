@@ -285,7 +285,7 @@ template <typename Params>
 cudaError_t launch_cluster(void (*kernel)(Params), SmemOptIn &opt_in, int words, const Params &p, int ctas,
                            cudaStream_t stream) {
     const size_t per = sizeof(int32_t) * (size_t)words, smem = per * (size_t)p.B;
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {   // 48 KB are free to use, the kernels' static arrays among them
         const cudaError_t e = opt_in.set(kernel, (int)(per * kMaxPagedBatch));
         if (e != cudaSuccess) return e;
     }
