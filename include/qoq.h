@@ -394,6 +394,8 @@ qoq_status qoq_kv4_decode_attention(const void *q_fp16, const uint8_t *k_codes, 
  * and of one layer's cache, for K and for V
  *   codes  uint8 [n_pages][Hkv][page_size][D/2], byte j = q[2j] | q[2j+1] << 4
  *   params FP16  [n_pages][Hkv][page_size][2], scale then zero
+ * as qoq_kv4_paged_write leaves them: scales >= 0, zeros whole numbers from 0 to 22
+ * (15, but for vectors whose scale is subnormal).
  * A token's slot is page * page_size + its offset in the page. page_size is
  * 16, 32, 64, 128 or 256, n_pages * page_size at most INT32_MAX.
  *

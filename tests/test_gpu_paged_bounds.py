@@ -6,7 +6,7 @@ import threading
 import numpy as np
 import pytest
 
-from gpu_helpers import host, torch
+from gpu_helpers import dev, host, torch
 from oracle import kv4_paged
 from paged_case import Batch, check, run
 from w4a8_quantized_gemm_qoq_b200 import qoq
@@ -111,3 +111,53 @@ def test_page_steps_of_many_requests(B):
     assert np.array_equal(host(pt.block_table), want["block_table"]) and int(host(pt.free_count)[0]) == 0
     pt.release(n)
     assert np.array_equal(host(pt.free_pages), free) and not host(pt.seq_lens).any() and pt.status() == 0
+
+
+U = 2.0 ** -24   # the smallest FP16 number, and the step of every scale below 2^-14
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("level", [-22, -37, -217, 22])
+def test_values_of_the_smallest_scales(page, new, level):
+    """Vectors whose scale is subnormal: its rounding makes zeros of up to 22 of
+    4-bit codes (-22 units: scale 1, zero 22, code 0)."""
+    b = Batch([90, 0, 300], [new, 3, 1], 8, 2, 128, page, seed=new)
+    for r in range(3):
+        t = np.arange(int(b.kv[r]))
+        x = np.full((len(t), 2, 128), level * U)
+        x[t % 5 == 4] = 3 * U
+        put(b, r, t, x, "v")
+    if level < 0:
+        assert (b.v_params[slots_of(b, 0, np.arange(90))][..., 1] > 15).any()
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("level", [-22, -37, -217])
+def test_keys_of_the_smallest_scales(page, new, level):
+    """The same among the keys, under queries so large that they count: scores
+    0.7 to 4 apart, and values of ordinary size that tell them apart."""
+    b = Batch([90, 0, 300], [new, 3, 1], 8, 2, 128, page, seed=new)
+    b.q[:] = min(50000.0, 4 / (-level * U * np.sqrt(128))) * (0.9 + 0.1 * np.tanh(b.q.astype(np.float64)))
+    for r in range(3):
+        t = np.arange(int(b.kv[r]))
+        x = np.zeros((len(t), 2, 128))
+        x[t % 3 == 0] = level * U
+        put(b, r, t, x, "k")
+    check(b, run(b))
+
+
+def test_smallest_scales_equal_contiguous_decode():
+    """One request of such keys and values in both caches: each decode call
+    within the bar."""
+    b = Batch([199], [1], 8, 2, 128, 16, seed=4)
+    rng = np.random.default_rng(4)
+    t = np.arange(200)
+    x = {n: (rng.choice([-22, -37, -217, 0, 5], (200, 2, 1)) * U * np.ones(128)).astype(np.float16) for n in "kv"}
+    for n in "kv":
+        put(b, 0, t, x[n], n)
+    kc, vc = (qoq.KV4Cache(1, 2, 200, 128).write(dev(np.ascontiguousarray(x[n].transpose(1, 0, 2))[None])) for n in "kv")
+    for got in (run(b), host(qoq.kv4_decode_attention(dev(b.q), kc, vc))):
+        check(b, got)

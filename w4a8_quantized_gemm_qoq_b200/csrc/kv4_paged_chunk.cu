@@ -1002,11 +1002,13 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 const uint32_t s = step_at + (uint32_t)(k - k0), stage = s & 1;
                 const uint32_t z = zeros + 4 * stage * 2 * kChKeys;
                 // The step's factors. A written scale is finite and a zero at
-                // most 15; the bounds make a hidden token's values
-                // so too, whatever it holds, so that its weight 0 stays 0.
+                // most 22 (15 times the 1.5 by which a subnormal scale may be
+                // rounded down); the bounds, 65504 and 30, make a hidden token's values
+                // finite, whatever it holds, so that its weight 0 stays 0. Up to 30
+                // 1024 + z, 64 + z and the codes' differences from them are exact.
                 const uint32_t sv = min(szv & 0xFFFFu, 0x7BFFu);
-                const float zk = fminf(fmaxf(__half2float(half_hi(szk)), 0.0f), 15.0f);
-                const float zv = fminf(fmaxf(__half2float(half_hi(szv)), 0.0f), 15.0f);
+                const float zk = fminf(fmaxf(__half2float(half_hi(szk)), 0.0f), 30.0f);
+                const float zv = fminf(fmaxf(__half2float(half_hi(szv)), 0.0f), 30.0f);
                 sts32(z + 4 * t, half2_bits(__floats2half2_rn(1024.0f + zk, 64.0f + zk)));
                 sts32(z + 4 * (kChKeys + t), half2_bits(__floats2half2_rn(1024.0f + zv, 64.0f + zv)));
                 const uint32_t wmax = __reduce_max_sync(0xffffffffu, sv);

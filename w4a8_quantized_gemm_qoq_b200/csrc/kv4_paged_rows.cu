@@ -546,10 +546,12 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                                (p.window == 0 || pos0 + r.n - 1 - t0 < p.window || t0 + kRwTile <= p.sinks);
             // The largest value scale (FP16 bits of values >= 0 are ordered),
             // and the tokens' factors for everyone. A written scale is finite
-            // and a zero at most 15; the bounds make the values' both so for
-            // whatever a hidden token may hold, so that its weight 0 stays 0.
+            // and a zero at most 22 (15 times the 1.5 by which a subnormal
+            // scale may be rounded down); the bounds, 65504 and 30, make the values'
+            // both finite for whatever a hidden token may hold, so that its
+            // weight 0 stays 0.
 #pragma unroll
-            for (int i = 0; i < 2; ++i) vw[i] = min(vw[i] & 0xFFFFu, 0x7BFFu) | (min(vw[i] >> 16, 0x4B80u) << 16);
+            for (int i = 0; i < 2; ++i) vw[i] = min(vw[i] & 0xFFFFu, 0x7BFFu) | (min(vw[i] >> 16, 0x4F80u) << 16);
             const uint32_t sv = __reduce_max_sync(0xffffffffu, max(vw[0] & 0xFFFFu, vw[1] & 0xFFFFu));
             const int ebn = max(eb, (int)(__float_as_uint(half_lo(sv)) >> 23));
             const float ef = __int_as_float((262 - ebn) << 23);   // 2^(8 - E)
