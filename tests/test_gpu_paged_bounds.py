@@ -161,3 +161,18 @@ def test_smallest_scales_equal_contiguous_decode():
     kc, vc = (qoq.KV4Cache(1, 2, 200, 128).write(dev(np.ascontiguousarray(x[n].transpose(1, 0, 2))[None])) for n in "kv")
     for got in (run(b), host(qoq.kv4_decode_attention(dev(b.q), kc, vc))):
         check(b, got)
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -13, 0.002, 2.0 ** -4])
+@pytest.mark.parametrize("window,sinks", [(50, 2), (1, 0), (1, 1), (130, 20)])
+@pytest.mark.parametrize("bad", [65504.0, np.inf, np.nan])
+def test_scales_of_hidden_tokens_do_not_matter(gain, window, sinks, bad):
+    """Tokens that no row sees hold huge, infinite or NaN scales beside small
+    visible values: the bound is that of the visible ones alone."""
+    b = Batch([400, 901, 130], [40, 1, 60], 8, 2, 128, 16, seed=9, gain=gain)
+    want = b.oracle(window, sinks)
+    for r in range(3):
+        t = np.arange(sinks, int(b.ctx[r]) - window + 1)
+        b.k_params[slots_of(b, r, t)] = bad if bad != 65504.0 else 1.0
+        b.v_params[slots_of(b, r, t)] = bad
+    check(b, run(b, window, sinks), want=want)

@@ -80,8 +80,10 @@ struct ChunkParams {
 };
 
 // The steps of a 256-row tile: sink steps [0, sinks), then [first, first + count - sinks).
+// Of their tokens some row sees those of [window, end) and the sinks before them.
 struct ChunkSteps {
     int sinks, first, count;
+    int window, end;
 };
 
 struct ChunkPiece {
@@ -107,6 +109,8 @@ __device__ __forceinline__ ChunkSteps chunk_steps(const PagedAttnParams &p, cons
     s.sinks = p.window ? min((min(p.sinks, w0) + kChKeys - 1) / kChKeys, s.first) : 0;
     s.count = p1 < 0 ? 0 : s.sinks + p1 / kChKeys + 1 - s.first;
     if (s.count == 0) s.sinks = 0;
+    s.window = w0;
+    s.end = p1 + 1;
     return s;
 }
 
@@ -948,14 +952,19 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                         from[i] + (uint64_t)min((uint32_t)g.chunk[i], last_page) * page_bytes + more));
             };
             uint32_t szk = 0u, szv = 0u;   // token t's scales and zeros
+            // What a token holds that no row of the tile sees must not matter: it
+            // counts as zero vectors.
+            const int seen_from = pc.st.window, seen_to = pc.st.end;
             auto load_sz = [&](int k, int page) {
                 szk = szv = 0u;
                 const int key = key_of(pc.st, k) + t;
                 if (k < k1 && key < kv) {
                     if ((uint32_t)page <= last_page) {
                         const int64_t at = from_t + (int64_t)page * page_vecs + (p.page_shift == 8 ? (key - t) & 128 : 0);
-                        szk = __ldg(reinterpret_cast<const uint32_t *>(p.k_params) + at);
-                        szv = __ldg(reinterpret_cast<const uint32_t *>(p.v_params) + at);
+                        if (key < seen_to && (key >= seen_from || key < p.sinks)) {
+                            szk = __ldg(reinterpret_cast<const uint32_t *>(p.k_params) + at);
+                            szv = __ldg(reinterpret_cast<const uint32_t *>(p.v_params) + at);
+                        }
                     } else {
                         paged_bad_request(p, pc.b);
                     }

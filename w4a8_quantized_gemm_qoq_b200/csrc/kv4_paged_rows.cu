@@ -76,6 +76,7 @@ constexpr float kRwSlack = 6.0f;              // log2 by which scores may exceed
 struct RowsParams {
     PagedAttnParams a;
     int g_inv;               // ceil(2^16 / G): c / G = c g_inv >> 16 for c < 64
+    int reach;               // the window, or INT32_MAX: a row sees the tokens less than so far before it
     int32_t *counters;       // [kRwResident], zero between calls
     float *part;             // [2 kRwResident][kRowsCols * D + 2 * kRowsCols]
     const int64_t *first;    // [B + 2] from the division kernel where B > kRwWarpBatch, else null
@@ -436,27 +437,32 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             }
             copy_commit();
         };
+        // Whether some row sees token t. What the others hold must not matter: in
+        // a tile that is walked for its neighbours they count as zero vectors.
+        auto seen = [&](int t) { return t < r.kv && (pos0 - t < w.reach || t < p.sinks); };
         // The scales and zeros of the lane's two tokens, (scale | zero << 16)
-        // each; 0 past the sequence's end and on bad pages.
+        // each; 0 where no row sees them and on bad pages.
         auto load_sz = [&](int k, int pg, uint32_t (&kw)[2], uint32_t (&vw)[2]) {
             const int t = tile_t0(k);
             kw[0] = kw[1] = vw[0] = vw[1] = 0u;
-            if (pg < 0 || t + tok0 >= r.kv) return;
+            if (pg < 0) return;
+            const bool in0 = seen(t + tok0), in1 = seen(t + tok1);
             const uint32_t vec = ((uint32_t)h << p.page_shift) + (SMALL ? (uint32_t)((t + tok0) & page_mask) : (uint32_t)((t & page_mask) + tok0));
             const uint8_t *at = reinterpret_cast<const uint8_t *>(p.k_params) +
                                 (((uint64_t)(uint32_t)pg * page_vecs + vec) << 2);
             if (SMALL) {
                 const uint2 kk = __ldg(reinterpret_cast<const uint2 *>(at));
                 const uint2 vv = __ldg(reinterpret_cast<const uint2 *>(at + vp_minus_kp));
-                kw[0] = kk.x, vw[0] = vv.x;
-                if (t + tok1 < r.kv) kw[1] = kk.y, vw[1] = vv.y;
+                if (in0) kw[0] = kk.x, vw[0] = vv.x;
+                if (in1) kw[1] = kk.y, vw[1] = vv.y;
             } else {
-                kw[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
-                vw[0] = __ldg(reinterpret_cast<const uint32_t *>(at + vp_minus_kp));
-                if (t + tok1 < r.kv) {
-                    kw[1] = __ldg(reinterpret_cast<const uint32_t *>(at + 128));
-                    vw[1] = __ldg(reinterpret_cast<const uint32_t *>(at + 128 + vp_minus_kp));
-                }
+                // All four at once: they lie in the page, seen or not.
+                const uint32_t k0 = __ldg(reinterpret_cast<const uint32_t *>(at));
+                const uint32_t v0 = __ldg(reinterpret_cast<const uint32_t *>(at + vp_minus_kp));
+                const uint32_t k1 = __ldg(reinterpret_cast<const uint32_t *>(at + 128));
+                const uint32_t v1 = __ldg(reinterpret_cast<const uint32_t *>(at + 128 + vp_minus_kp));
+                if (in0) kw[0] = k0, vw[0] = v0;
+                if (in1) kw[1] = k1, vw[1] = v1;
             }
         };
 
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             if (k + kRwWarps < k_end) load_sz(k + kRwWarps, pgn, kwn, vwn);   // in flight while this tile is computed
             // Whether every column sees every token of the tile.
             const bool whole = t0 + kRwTile - 1 <= pos0 &&
-                               (p.window == 0 || pos0 + r.n - 1 - t0 < p.window || t0 + kRwTile <= p.sinks);
+                               (pos0 + r.n - 1 - t0 < w.reach || t0 + kRwTile <= p.sinks);
             // The largest value scale (FP16 bits of values >= 0 are ordered),
             // and the tokens' factors for everyone. A written scale is finite
             // and a zero at most 22 (15 times the 1.5 by which a subnormal
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int t = t0 + 16 * j + gid + (c >> 1) * 8, d = cpos[c & 1] - t;
-                        if (!(d >= 0 && (p.window == 0 || d < p.window || t < p.sinks))) sc[j][c] = -INFINITY;
+                        if (!(d >= 0 && (d < w.reach || t < p.sinks))) sc[j][c] = -INFINITY;
                     }
             }
             __syncwarp();   // every lane is done with the keys: the next tile's values take their place
@@ -898,6 +904,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cud
     RowsParams w;
     w.a = p;
     w.g_inv = (65536 + p.G - 1) / p.G;
+    w.reach = p.window ? p.window : INT32_MAX;
     uint8_t *at = static_cast<uint8_t *>(ws);
     w.counters = reinterpret_cast<int32_t *>(at);
     at += align256(4 * kRwResident);
