@@ -8,7 +8,7 @@ import pytest
 
 from gpu_helpers import dev, host, torch
 from oracle import kv4_paged
-from paged_case import Batch, check, run
+from paged_case import Batch, check, run, workspace
 from w4a8_quantized_gemm_qoq_b200 import qoq
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
@@ -176,3 +176,43 @@ def test_scales_of_hidden_tokens_do_not_matter(gain, window, sinks, bad):
         b.k_params[slots_of(b, r, t)] = bad if bad != 65504.0 else 1.0
         b.v_params[slots_of(b, r, t)] = bad
     check(b, run(b, window, sinks), want=want)
+
+
+def _hide(b, window, sinks, number):
+    """Entries of pages without a visible token become `number`."""
+    for r in range(len(b.ctx)):
+        first = max(0, int(b.ctx[r]) - window + 1)   # of the first row's window
+        for i in range(-(-int(b.kv[r]) // b.page)):
+            if sinks <= i * b.page and (i + 1) * b.page <= first:
+                b.table[r, i] = number
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(100, 0), (100, 4), (77, 70), (1, 1)])
+@pytest.mark.parametrize("number", [-1, 10 ** 6])
+def test_pages_without_visible_tokens_may_be_taken_back(page, window, sinks, number):
+    """Pages between the sinks and the window are no longer in the table:
+    no request is refused, the outputs are those of the full table."""
+    b = Batch([1000, 611, 0, 2050, 333], [1, 5, 300, 90, 17], 8, 2, 128, page, seed=page)
+    want = b.oracle(window, sinks)
+    _hide(b, window, sinks, number)
+    assert (b.table[:, :2] != -1).any()
+    check(b, run(b, window, sinks), want=want)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("where", ["sinks", "window"])
+def test_a_page_with_one_visible_token_is_checked(page, new, where):
+    """The page that holds the first token of the window, its last one, or the last sink:
+    a bad entry names the request."""
+    ctx = 20 * page + 99   # the first row's window begins with the last token of page 20
+    window, sinks = 100 - page + 1, 3 * page + 1
+    b = Batch([50, ctx], [1, new], 8, 2, 128, page, seed=page)
+    assert (ctx - window + 1) == 21 * page - 1
+    entry = 3 if where == "sinks" else 20
+    b.table[1, entry] = -1
+    ws = workspace(b)
+    qoq.kv4_paged_attention(dev(b.q), b.cache(), dev(b.table), dev(b.q_start), dev(b.kv), new, window=window, sinks=sinks,
+                            ws=ws)
+    assert ws.status() == 1 and ws.timeout_site()[0] == 1

@@ -953,18 +953,16 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             };
             uint32_t szk = 0u, szv = 0u;   // token t's scales and zeros
             // What a token holds that no row of the tile sees must not matter: it
-            // counts as zero vectors.
+            // counts as zero vectors, and its page may have been taken back.
             const int seen_from = pc.st.window, seen_to = pc.st.end;
             auto load_sz = [&](int k, int page) {
                 szk = szv = 0u;
                 const int key = key_of(pc.st, k) + t;
-                if (k < k1 && key < kv) {
+                if (k < k1 && key < seen_to && (key >= seen_from || key < p.sinks)) {
                     if ((uint32_t)page <= last_page) {
                         const int64_t at = from_t + (int64_t)page * page_vecs + (p.page_shift == 8 ? (key - t) & 128 : 0);
-                        if (key < seen_to && (key >= seen_from || key < p.sinks)) {
-                            szk = __ldg(reinterpret_cast<const uint32_t *>(p.k_params) + at);
-                            szv = __ldg(reinterpret_cast<const uint32_t *>(p.v_params) + at);
-                        }
+                        szk = __ldg(reinterpret_cast<const uint32_t *>(p.k_params) + at);
+                        szv = __ldg(reinterpret_cast<const uint32_t *>(p.v_params) + at);
                     } else {
                         paged_bad_request(p, pc.b);
                     }

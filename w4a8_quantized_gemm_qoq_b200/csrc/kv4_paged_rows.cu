@@ -411,7 +411,10 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         };
         // The page of the lane's tokens of tile k, as the table has it (-1 past the
         // sequence's end). It is looked at a tile later, when it has arrived:
-        // `checked` makes -1 of a number outside the cache and names the request.
+        // `checked` makes -1 of a number outside the cache, and names the request if
+        // some row sees a token of that page in the tile: entries of pages
+        // behind the sinks and before the window may have been taken back. (In
+        // large pages a tile is walked only if a row sees some of it.)
         const int32_t *table = p.block_table + (int64_t)b * p.max_pages;
         auto load_page = [&](int k) {
             const int t = tile_t0(k) + part;
@@ -419,7 +422,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         };
         auto checked = [&](int k, int pg) {
             if ((uint32_t)pg < (uint32_t)p.n_pages) return pg;
-            if (k < k_end && tile_t0(k) + part < r.kv) paged_bad_request(p, b);
+            const int t = tile_t0(k) + part;
+            if (k < k_end && t < r.kv && (!SMALL || pos0 - (t + 15) < w.reach || t < p.sinks)) paged_bad_request(p, b);
             return -1;
         };
         // Tile k's codes into the ring at `dst` as one copy group (empty past
