@@ -216,3 +216,31 @@ def test_a_page_with_one_visible_token_is_checked(page, new, where):
     qoq.kv4_paged_attention(dev(b.q), b.cache(), dev(b.table), dev(b.q_start), dev(b.kv), new, window=window, sinks=sinks,
                             ws=ws)
     assert ws.status() == 1 and ws.timeout_site()[0] == 1
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,G", [(1, 4), (5, 8), (3, 1), (100, 4)])
+def test_queries_of_the_smallest_numbers(D, new, G):
+    """Queries of a few units of 2^-24 under keys of 60000: scores of ordinary
+    size, which an eighth of a unit lost per dim would change."""
+    b = Batch([60, 0, 300], [new, new, 1], 2 * G, 2, D, 64, seed=D + new)
+    rng = np.random.default_rng(D)
+    b.q[:] = rng.integers(1, 40, b.q.shape) * U
+    for r in range(3):
+        t = np.arange(int(b.kv[r]))
+        put(b, r, t, np.broadcast_to((rng.integers(-1, 2, (len(t), 2, 1)) * 60000.0), (len(t), 2, D)).copy(), "k")
+    check(b, run(b))
+
+
+def test_queries_of_different_sizes_side_by_side():
+    """Heads and rows from 2^-24 to 2^10 in one product: each meets the bar."""
+    b = Batch([70, 500], [3, 1], 16, 2, 128, 64, seed=6)
+    e = np.arange(b.rows * 16).reshape(b.rows, 16)
+    b.q[:] = b.q.astype(np.float64) * 2.0 ** -(e % 15)[..., None]
+    b.q[0, 3], b.q[1, 5], b.q[2, 7, ::2] = 0, np.float16(U), 0
+    b.q[3, 9] *= np.float16(2.0 ** 9)
+    for r in range(2):
+        t = np.arange(int(b.kv[r]))
+        at = slots_of(b, r, t)
+        b.k_params[at + (0,)] = (b.k_params[at + (0,)].astype(np.float64) / 256).astype(np.float16)
+    check(b, run(b))

@@ -492,35 +492,62 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         // d + 2b, d + 2b + 1), k-step 2 i takes the low nibbles, pairing dims
         // (d, d+4) and (d+2, d+6), k-step 2 i + 1 the high nibbles, pairing
         // (d+1, d+5) and (d+3, d+7).
+        //
+        // The queries that meet high nibbles are divided by 16 as FP16. So that
+        // small ones lose nothing by it, every column is first multiplied by a power of two
+        // that brings its largest component to 2^15 or more (a subnormal one
+        // to 2^5 times its units): what the division then rounds is below 2^-36 of
+        // that component. The scores' exponentials take the power back.
         uint32_t qf[KS][2];
-        float sq2[2];
+        float sq2[2], cs[2];   // sum of dims, for the zero points, and 2^-k, of columns 2 tig, 2 tig + 1
         {
             const int col = col0 + gid, i0 = (col * w.g_inv) >> 16;   // i0 = col / G
             const __half *qrow = p.q + (int64_t)(r.row0 + i0) * p.q_stride +
                                  (int64_t)(h * p.G + col - i0 * p.G) * D + tig * (D / 4);
+            uint4 u[KW];
+            __half2 top = __floats2half2_rn(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+                u[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (gid < cols) u[i] = __ldg(reinterpret_cast<const uint4 *>(qrow + 8 * i));
+                const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(*reinterpret_cast<const __half2 *>(&uw[e])));
+            }
+            uint32_t tb = half2_bits(top);
+            tb = max(tb & 0xFFFFu, tb >> 16);   // FP16 bits of values >= 0 are ordered
+            tb = max(tb, __shfl_xor_sync(0xffffffffu, tb, 1));
+            tb = max(tb, __shfl_xor_sync(0xffffffffu, tb, 2));
+            const int k2 = tb >= 0x7C00u ? 0 : 30 - max((int)(tb >> 10), 1);   // 2^k2 in two factors that FP16 holds
+            const __half2 up0 = __float2half2_rn(__int_as_float((127 + min(k2, 15)) << 23));
+            const __half2 up1 = __float2half2_rn(__int_as_float((127 + max(k2 - 15, 0)) << 23));
             const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
             float sq = 0.0f;
 #pragma unroll
             for (int i = 0; i < KW; ++i) {
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (gid < cols) u = __ldg(reinterpret_cast<const uint4 *>(qrow + 8 * i));
-                qf[2 * i][0] = __byte_perm(u.x, u.z, 0x5410);
-                qf[2 * i][1] = __byte_perm(u.y, u.w, 0x5410);
-                // High nibbles enter 16 times too large.
-                const uint32_t h0 = __byte_perm(u.x, u.z, 0x7632), h1 = __byte_perm(u.y, u.w, 0x7632);
-                qf[2 * i + 1][0] = half2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&h0), sixteenth));
-                qf[2 * i + 1][1] = half2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&h1), sixteenth));
-                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+                uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&uw[e]));
+                    const __half2 q2 = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&uw[e]), up0), up1);
+                    uw[e] = half2_bits(q2);
+                    const float2 f = __half22float2(q2);
                     sq += f.x + f.y;
                 }
+                qf[2 * i][0] = __byte_perm(uw[0], uw[2], 0x5410);
+                qf[2 * i][1] = __byte_perm(uw[1], uw[3], 0x5410);
+                // High nibbles enter 16 times too large.
+                const uint32_t h0 = __byte_perm(uw[0], uw[2], 0x7632), h1 = __byte_perm(uw[1], uw[3], 0x7632);
+                qf[2 * i + 1][0] = half2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&h0), sixteenth));
+                qf[2 * i + 1][1] = half2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&h1), sixteenth));
             }
             sq += __shfl_xor_sync(0xffffffffu, sq, 1);
-            sq += __shfl_xor_sync(0xffffffffu, sq, 2);            // column gid's sum of dims, for the zero points
-            sq2[0] = __shfl_sync(0xffffffffu, sq, 8 * tig);       // column 2 tig
-            sq2[1] = __shfl_sync(0xffffffffu, sq, 8 * tig + 4);   // column 2 tig + 1
+            sq += __shfl_xor_sync(0xffffffffu, sq, 2);            // column gid's
+            const float down = __int_as_float((127 - k2) << 23);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sq2[c] = __shfl_sync(0xffffffffu, sq, 8 * tig + 4 * c);
+                cs[c] = __shfl_sync(0xffffffffu, down, 8 * tig + 4 * c);
+            }
         }
         // Positions of the lane's two columns; columns >= cols see every token.
         int cpos[2];
@@ -577,7 +604,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             copy_wait<2>();   // this tile's keys have landed
             __syncwarp();
             // 1. Scores (tokens x columns) of the tile's four 16-token steps:
-            // s c (2^24 acc - z sum(q)).
+            // s c (2^24 acc - z sum(q)), times the column's 2^k.
             float sc[4][4];
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {   // two steps' chains of products side by side
@@ -643,7 +670,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             // 2. Online softmax over the whole tile. The running maximum
             // starts at a finite value below every score, so a column that
             // sees nothing keeps p = 2^-inf = 0.
-            float mx[2] = {m2[0], m2[1]};
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 mx[0] = fmaxf(mx[0], fmaxf(sc[j][0], sc[j][2]));
@@ -654,6 +681,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                 mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], s));
                 mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], s));
             }
+            mx[0] *= cs[0];
+            mx[1] *= cs[1];
             const bool raise = mx[0] > m2[0] + kRwSlack || mx[1] > m2[1] + kRwSlack;
             if (__any_sync(0xffffffffu, raise || ebn != eb)) {
                 const float es = __int_as_float((127 + eb - ebn) << 23);   // 2^(E_old - E_new)
@@ -683,7 +712,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                 float pr[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    pr[c] = ex2_approx(sc[j][c] - m2[c & 1]);
+                    pr[c] = ex2_approx(fmaf(sc[j][c], cs[c & 1], -m2[c & 1]));
                     l2[c & 1] += pr[c];   // this lane's tokens; summed over the lanes at the end
                 }
                 sts32(pt_st + (uint32_t)(16 * j * 16), half2_bits(__floats2half2_rn(pr[0] * svA, pr[1] * svA)));
