@@ -244,3 +244,19 @@ def test_queries_of_different_sizes_side_by_side():
         at = slots_of(b, r, t)
         b.k_params[at + (0,)] = (b.k_params[at + (0,)].astype(np.float64) / 256).astype(np.float16)
     check(b, run(b))
+
+
+@pytest.mark.parametrize("ctx,new", [([300, 40], [1, 1]), ([5000], [3]), ([200, 0], [100, 70]), ([4000], [60])])
+@pytest.mark.parametrize("what", [np.nan, np.inf])
+def test_queries_that_are_not_numbers(ctx, new, what):
+    """A NaN or infinite component of a query: that row and head's outputs are
+    not numbers, the others are as without it."""
+    b = Batch(ctx, new, 8, 2, 128, 64, seed=5)
+    want = b.oracle()
+    i, h = b.rows - 1, 5
+    b.q[i, h, 17] = what
+    out = run(b)
+    assert np.isnan(out[i, h]).all()
+    err = np.abs(out.astype(np.float64) - want[0]).max(axis=2)
+    err[i, h] = 0
+    assert (err <= 2.0 ** -10 * want[1] + 2.0 ** -24).all()

@@ -814,13 +814,15 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             }
             return sum;
         };
+        // A sum of 0 is that of a row which sees nothing; one that is no number (a
+        // query or a visible key was none) makes the outputs none.
         auto store_out = [&](int i, const float4 &v, float L) {
             const int c = seg.col0 + 4 * i / D, i0 = (c * w.g_inv) >> 16;   // i0 = c / G
             const float x[4] = {v.x, v.y, v.z, v.w};
             uint32_t h2[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                h2[e] = half2_bits(L > 0.0f ? __floats2half2_rn(x[2 * e] / L, x[2 * e + 1] / L) : __floats2half2_rn(0.0f, 0.0f));
+                h2[e] = half2_bits(L == 0.0f ? __floats2half2_rn(0.0f, 0.0f) : __floats2half2_rn(x[2 * e] / L, x[2 * e + 1] / L));
             *reinterpret_cast<uint2 *>(p.out + (int64_t)(seg.row0 + i0) * p.out_stride +
                                        (int64_t)(seg.h * p.G + c - i0 * p.G) * D + 4 * i % D) = make_uint2(h2[0], h2[1]);
         };
