@@ -493,7 +493,9 @@ qoq_status qoq_kv4_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int6
  * times the value scales are rounded to FP16 for the product with the value
  * codes, and the output is rounded once, so |o - o*| <= 2^-10 max|v| + 2^-24
  * per row and head, with max|v| over the request's visible tokens. The cached
- * values of the tokens that no row sees do not matter, whatever they hold.
+ * values of the tokens that no row sees do not matter, whatever they hold. A
+ * row whose query, or a visible token whose scale, is infinite or NaN gives
+ * outputs that are NaN.
  *
  * max_new: an upper bound of n_b known on the host (1 for a decode step); it
  * selects the kernels. kv_lens and q_start are clamped to what the buffers

@@ -260,3 +260,24 @@ def test_queries_that_are_not_numbers(ctx, new, what):
     err = np.abs(out.astype(np.float64) - want[0]).max(axis=2)
     err[i, h] = 0
     assert (err <= 2.0 ** -10 * want[1] + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("ctx,new", [([300, 40], [1, 1]), ([5000], [3]), ([200, 0], [100, 70]), ([4000], [60])])
+@pytest.mark.parametrize("tensor", ["k", "v"])
+@pytest.mark.parametrize("what", [np.nan, np.inf])
+def test_visible_scales_that_are_not_numbers(ctx, new, tensor, what):
+    """A token whose scale is infinite or NaN: the outputs of the rows that see
+    it are not numbers, in its KV head alone; rows that do not see it are clean."""
+    b = Batch(ctx, new, 8, 2, 128, 64, seed=7)
+    window, sinks = 90, 3
+    want = b.oracle(window, sinks)
+    n, kv = int(b.new[0]), int(b.kv[0])
+    at = kv - 1 - n // 2
+    (b.k_params if tensor == "k" else b.v_params)[b.table[0, at // 64], 1, at % 64, 0] = what
+    out = run(b, window, sinks)
+    seen = np.zeros((b.rows, 8), bool)
+    for i in range(n):
+        seen[i, 4:] = kv4_paged.visible(kv - n + i, kv, window, sinks)[at]
+    assert seen.any() and np.isnan(out[seen]).all()
+    err = np.abs(out.astype(np.float64) - want[0]).max(axis=2)
+    assert (err[~seen] <= (2.0 ** -10 * want[1] + 2.0 ** -24)[~seen]).all()

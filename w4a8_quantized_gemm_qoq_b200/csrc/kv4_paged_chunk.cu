@@ -1010,8 +1010,10 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 const uint32_t z = zeros + 4 * stage * 2 * kChKeys;
                 // The step's factors. A written scale is finite and a zero at
                 // most 22 (15 times the 1.5 by which a subnormal scale may be
-                // rounded down); the bounds, 65504 and 30, make a hidden token's values
-                // finite, whatever it holds, so that its weight 0 stays 0. Up to 30
+                // rounded down); the bounds, 65504 and 30, make the values finite for whatever
+                // a token that some rows do not see may hold, so that its weight 0 stays 0. A
+                // scale that is not finite makes the score NaN instead, and so
+                // the outputs of the rows that see the token. Up to 30
                 // 1024 + z, 64 + z and the codes' differences from them are exact.
                 const uint32_t sv = min(szv & 0xFFFFu, 0x7BFFu);
                 const float zk = fminf(fmaxf(__half2float(half_hi(szk)), 0.0f), 30.0f);
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 const uint32_t f = factors + 4 * ((s & 3) * 2 * kChKeys + t);
                 const uint32_t top = max(max(emax_s[stage][0], emax_s[stage][1]), max(emax_s[stage][2], emax_s[stage][3]));
                 const int ebn = max(eb, (int)(__float_as_uint(half_lo(top)) >> 23));
-                sts32f(f, half_lo(szk) * p.qscale);
+                sts32f(f, max(szk & 0xFFFFu, szv & 0xFFFFu) > 0x7BFFu ? __int_as_float(0x7FFFFFFF) : half_lo(szk) * p.qscale);
                 sts32f(f + 4 * kChKeys, half_lo(sv) * __int_as_float((262 - ebn) << 23));   // 2^(8 - E)
                 if (t == 0) {
                     es_s[s & 3] = __int_as_float((127 + eb - ebn) << 23);

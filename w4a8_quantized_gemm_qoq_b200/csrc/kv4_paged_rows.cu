@@ -585,8 +585,11 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             // and the tokens' factors for everyone. A written scale is finite
             // and a zero at most 22 (15 times the 1.5 by which a subnormal
             // scale may be rounded down); the bounds, 65504 and 30, make the values'
-            // both finite for whatever a hidden token may hold, so that its
-            // weight 0 stays 0.
+            // both finite for whatever a token that some rows do not see may hold,
+            // so that its weight 0 stays 0. A scale that is not finite makes the
+            // score NaN instead, and so the outputs of the rows that see the token.
+#pragma unroll
+            for (int i = 0; i < 2; ++i) kw[i] = max(kw[i] & 0xFFFFu, vw[i] & 0xFFFFu) > 0x7BFFu ? 0x7E00u : kw[i];
 #pragma unroll
             for (int i = 0; i < 2; ++i) vw[i] = min(vw[i] & 0xFFFFu, 0x7BFFu) | (min(vw[i] >> 16, 0x4F80u) << 16);
             const uint32_t sv = __reduce_max_sync(0xffffffffu, max(vw[0] & 0xFFFFu, vw[1] & 0xFFFFu));
