@@ -281,3 +281,22 @@ def test_visible_scales_that_are_not_numbers(ctx, new, tensor, what):
     assert seen.any() and np.isnan(out[seen]).all()
     err = np.abs(out.astype(np.float64) - want[0]).max(axis=2)
     assert (err[~seen] <= (2.0 ** -10 * want[1] + 2.0 ** -24)[~seen]).all()
+
+
+@pytest.mark.parametrize("ctx,new", [([30], [1]), ([30], [40]), ([3000], [60])])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_an_infinite_query_under_keys_of_one_sign(ctx, new, sign):
+    """Every score of the row is -infinity, or every one +infinity: a softmax of
+    either has no value."""
+    b = Batch(ctx, new, 8, 2, 128, 64, seed=8)
+    t = np.arange(int(b.kv[0]))
+    x = np.random.default_rng(8).standard_normal((len(t), 2, 128))
+    x[:, :, 17] = sign * 4
+    put(b, 0, t, x, "k")
+    want = b.oracle()
+    b.q[0, 2, 17] = np.inf
+    out = run(b)
+    assert np.isnan(out[0, 2]).all()
+    err = np.abs(out.astype(np.float64) - want[0]).max(axis=2)
+    err[0, 2] = 0
+    assert (err <= 2.0 ** -10 * want[1] + 2.0 ** -24).all()

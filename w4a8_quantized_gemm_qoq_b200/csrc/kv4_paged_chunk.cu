@@ -853,7 +853,9 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
             __syncwarp();
             const float row_max = stats_s[warp][lane].x, row_sum = stats_s[warp][lane].y;
             __syncwarp();
-            const float f = slot >= 0 ? unit : row_sum > 0.0f ? unit / row_sum : 0.0f;
+            // A row before the sequence sees nothing and gives zeros. Every other one
+            // sees itself: without a sum its scores were all -infinity, and 0 / 0 says so.
+            const float f = slot >= 0 ? unit : r.kv - r.n + token < 0 ? 0.0f : unit / row_sum;
             __half *out = p.out + (int64_t)(r.row0 + token) * p.out_stride + (int64_t)head * D;
             float *part_o = w.part + ((int64_t)slot * w.slot_rows + wg * 128 + row) * D;
 #pragma unroll
@@ -1182,8 +1184,8 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_kernel(const __grid_consta
             }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-            const float f = l > 0.0f ? 1.0f / l : 0.0f;
             const int pair = it.z * kChRows + row, token = pair / p.G;
+            const float f = r.kv - r.n + token < 0 ? 0.0f : 1.0f / l;   // as for undivided items
             __half2 *out = reinterpret_cast<__half2 *>(p.out + (int64_t)(r.row0 + token) * p.out_stride +
                                                        (int64_t)(it.y * p.G + pair - token * p.G) * D + lane * (D / 32));
 #pragma unroll
