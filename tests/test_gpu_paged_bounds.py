@@ -300,3 +300,15 @@ def test_an_infinite_query_under_keys_of_one_sign(ctx, new, sign):
     err = np.abs(out.astype(np.float64) - want[0]).max(axis=2)
     err[0, 2] = 0
     assert (err <= 2.0 ** -10 * want[1] + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("B,top,window", [(8, 16, 0), (3, 100, 0), (20, 13, 200)])
+def test_a_padded_batch_of_few_rows(B, top, window):
+    """A step with room for `top` rows of every request serves requests of few:
+    the bits are those of the step without that room."""
+    b = Batch([(0, 61, 500, 3, 260)[i % 5] for i in range(B)], [1 + i % 3 for i in range(B)], 8, 2, 128, 64, seed=B)
+    want = run(b, window, 4)
+    b.q = np.concatenate([b.q, np.zeros((B * top - len(b.q),) + b.q.shape[1:], np.float16)])
+    got = run(b, window, 4, max_new=top)
+    check(b, got, window, 4)
+    assert np.array_equal(got[:b.rows].view(np.uint16), want[:b.rows].view(np.uint16))

@@ -14,18 +14,18 @@ size_t kv4_paged_workspace_bytes(int64_t B, int64_t, int64_t Hq, int64_t Hkv, in
 // kernel, the others to the many-rows one. Measured on both sides of it, 32 sequences
 // of 1500 to 4500 tokens, 8 KV heads of 128: with 8, 16, 24, 32, 40, 48 and 64
 // pairs the former takes 34, 52, 70, 86, 104, 122 and 157 us, the latter
-// 127 to 132 us with 16 to 64 of them. Where
-// every request has max_new rows (as N says it may) and those are many, the
-// few-rows kernel would find nothing, and the other takes whatever comes.
+// 127 to 132 us with 16 to 64 of them. Which requests have few rows is known on the
+// device only: N and max_new are what the buffers have room for. So where
+// some may have many, both kernels run. Where all of them do, the few-rows kernel
+// finds nothing, which costs 1 to 2 us (a prompt of 100 in 20.4 us, of 4096 in 234.2, without
+// it 19.4 and 232.0); without it 32 decoding requests in a step with room for
+// 16 rows each take 121 us, not 38.7, and 5 drafted tokens of each 126, not 76.
 cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws,
                                    cudaStream_t stream) {
     uint8_t *at = static_cast<uint8_t *>(ws) + 256;
-    const bool many = max_new * p.G > kRowsMax, all = many && p.N >= p.B * max_new;
-    if (!all) {
-        const cudaError_t e = launch_paged_rows(p, D, at, stream);
-        if (e != cudaSuccess || !many) return e;
-    }
-    return launch_paged_chunk(p, D, all ? 0 : kRowsMax, max_new, at + rows_workspace_bytes(p.B, D), stream);
+    const cudaError_t e = launch_paged_rows(p, D, at, stream);
+    if (e != cudaSuccess || max_new * p.G <= kRowsMax) return e;
+    return launch_paged_chunk(p, D, max_new, at + rows_workspace_bytes(p.B, D), stream);
 }
 
 }  // namespace qoq

@@ -71,7 +71,6 @@ constexpr int kDvThreads = 1024;
 
 struct ChunkParams {
     PagedAttnParams a;
-    int rows_limit;      // requests with at most so many (row, head) pairs per KV head belong to the few-rows kernel
     int slot_rows;       // rows of a partial result
     int32_t *division;   // by place in the order: start[B + 1], slot[B + 1] (pieces and divided pieces before),
                          // parts[B] (per item), request[B]
@@ -95,9 +94,10 @@ struct ChunkPiece {
     ChunkSteps st;
 };
 
+// (row, head) pairs per KV head of a request for this kernel, else 0.
 __device__ __forceinline__ int chunk_rows(const ChunkParams &w, const PagedRequest &r) {
     const int rows = r.n * w.a.G;
-    return r.n > w.a.max_new || rows <= w.rows_limit ? 0 : rows;
+    return r.n > w.a.max_new || rows <= kRowsMax ? 0 : rows;
 }
 
 __device__ __forceinline__ ChunkSteps chunk_steps(const PagedAttnParams &p, const PagedRequest &r, int tile) {
@@ -1202,8 +1202,7 @@ int slot_rows(int64_t max_new, int64_t G) {
 // A launch that may begin before the kernel ahead of it has ended, whose results
 // it waits for itself.
 template <typename Kernel>
-cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, const ChunkParams &w, cudaStream_t stream,
-                             bool dependent = true) {
+cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, const ChunkParams &w, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
@@ -1213,7 +1212,7 @@ cudaError_t launch_dependent(Kernel kernel, int blocks, int threads, int smem, c
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = dependent ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, w);
 }
 
@@ -1224,8 +1223,8 @@ cudaError_t launch(const ChunkParams &w, cudaStream_t stream) {
     cudaError_t e = opt_in.set(kv4_chunk_kernel<D>, smem);
     if (e != cudaSuccess) return e;
     const int threads = w.a.B >= kDvThreads ? kDvThreads : (w.a.B + 31) / 32 * 32;
-    // Beside the few-rows kernel, where that runs: it reads nothing that one writes.
-    e = launch_dependent(kv4_chunk_division_kernel, 1, threads, 0, w, stream, w.rows_limit > 0);
+    // Beside the few-rows kernel: it reads nothing that one writes.
+    e = launch_dependent(kv4_chunk_division_kernel, 1, threads, 0, w, stream);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kv4_chunk_kernel<D>, kChCtas, kChThreads, smem, w, stream);
     if (e != cudaSuccess) return e;
@@ -1240,12 +1239,10 @@ size_t chunk_workspace_bytes(int64_t B, int64_t max_new, int64_t G, int64_t D) {
            (size_t)align256((int64_t)4 * kChSlots * slot_rows(max_new, G) * (D + 2));
 }
 
-// Requests with more than rows_limit (row, head) pairs per KV head.
-cudaError_t launch_paged_chunk(const PagedAttnParams &p, int64_t D, int rows_limit, int64_t max_new, void *ws,
-                               cudaStream_t stream) {
+// Requests with more than kRowsMax (row, head) pairs per KV head, behind launch_paged_rows.
+cudaError_t launch_paged_chunk(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws, cudaStream_t stream) {
     ChunkParams w;
     w.a = p;
-    w.rows_limit = rows_limit;
     w.slot_rows = slot_rows(max_new, p.G);
     uint8_t *at = static_cast<uint8_t *>(ws);
     w.division = reinterpret_cast<int32_t *>(at);

@@ -192,8 +192,7 @@ constexpr int kRowsCols = 8;   // of which one piece takes so many, the columns 
 size_t rows_workspace_bytes(int64_t B, int64_t D);
 cudaError_t launch_paged_rows(const PagedAttnParams &p, int64_t D, void *ws, cudaStream_t stream);
 size_t chunk_workspace_bytes(int64_t B, int64_t max_new, int64_t G, int64_t D);
-cudaError_t launch_paged_chunk(const PagedAttnParams &p, int64_t D, int rows_limit, int64_t max_new, void *ws,
-                               cudaStream_t stream);
+cudaError_t launch_paged_chunk(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws, cudaStream_t stream);
 size_t kv4_paged_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_new);
 cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws,
                                    cudaStream_t stream);
