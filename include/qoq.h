@@ -518,7 +518,10 @@ qoq_status qoq_kv4_paged_read(const int32_t *slots, int64_t N, int64_t Hkv, int6
  * piece, and the outputs are undefined),
  * control words that every call leaves zero, then scratch; calls that may
  * overlap on the device need separate workspaces. The size depends on B, N,
- * the heads and max_new, not on the lengths.
+ * the heads and max_new, not on the lengths. The control words lie at one place
+ * whatever the sizes: a workspace serves any calls of this function, one after another,
+ * whose sizes it covers. It does not serve other functions, whose scratch
+ * may lie over these control words.
  */
 qoq_status qoq_kv4_paged_attention(const void *q_fp16, int64_t q_stride, const uint8_t *k_codes,
                                    const void *k_params, const uint8_t *v_codes, const void *v_params,

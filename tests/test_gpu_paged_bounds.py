@@ -312,3 +312,16 @@ def test_a_padded_batch_of_few_rows(B, top, window):
     got = run(b, window, 4, max_new=top)
     check(b, got, window, 4)
     assert np.array_equal(got[:b.rows].view(np.uint16), want[:b.rows].view(np.uint16))
+
+
+def test_one_workspace_for_calls_of_different_shapes():
+    """Batches, head sizes and row bounds that lay the scratch out differently,
+    one after another in one workspace: the bits of calls with their own."""
+    shapes = [([300] * 200, [1] * 200, 4, 1, 64), ([5000], [1], 8, 2, 128), ([100, 0], [200, 3], 8, 2, 128),
+              ([7] * 130, [30] * 130, 4, 1, 64), ([9000, 20], [1, 40], 8, 8, 128), ([20000], [2], 8, 1, 64)]
+    batches = [Batch(c, n, Hq, Hkv, D, 64, seed=i) for i, (c, n, Hq, Hkv, D) in enumerate(shapes)]
+    big = qoq.Workspace(max(workspace(b).buf.numel() for b in batches))
+    for _ in range(2):
+        for b in batches + batches[::-1]:
+            got = run(b, ws=big)
+            assert np.array_equal(got.view(np.uint16), run(b).view(np.uint16))
