@@ -325,3 +325,19 @@ def test_one_workspace_for_calls_of_different_shapes():
         for b in batches + batches[::-1]:
             got = run(b, ws=big)
             assert np.array_equal(got.view(np.uint16), run(b).view(np.uint16))
+
+
+@pytest.mark.parametrize("ctx,new", [([300, 40], [1, 1]), ([200, 0], [100, 70])])
+def test_negative_zeros_among_the_parameters(ctx, new):
+    """A cache filled by other means may hold -0 as a zero or a scale: 0."""
+    b = Batch(ctx, new, 8, 2, 128, 64, seed=2)
+    rng = np.random.default_rng(2)
+    for r in range(2):
+        t = np.arange(int(b.kv[r]))
+        for name in "kv":
+            put(b, r, t, np.abs(rng.standard_normal((len(t), 2, 128))), name)
+            put(b, r, t[::5], np.zeros((len(t[::5]), 2, 128)), name)
+    want = b.oracle()
+    for params in (b.k_params, b.v_params):
+        params[params == 0] = np.float16(-0.0)
+    check(b, run(b), want=want)

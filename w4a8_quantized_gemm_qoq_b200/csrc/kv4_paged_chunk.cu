@@ -1012,12 +1012,12 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 const uint32_t z = zeros + 4 * stage * 2 * kChKeys;
                 // The step's factors. A written scale is finite and a zero at
                 // most 22 (15 times the 1.5 by which a subnormal scale may be
-                // rounded down); the bounds, 65504 and 30, make the values finite for whatever
-                // a token that some rows do not see may hold, so that its weight 0 stays 0. A
-                // scale that is not finite makes the score NaN instead, and so
-                // the outputs of the rows that see the token. Up to 30
-                // 1024 + z, 64 + z and the codes' differences from them are exact.
-                const uint32_t sv = min(szv & 0xFFFFu, 0x7BFFu);
+                // rounded down); up to 30 1024 + z, 64 + z and the codes' differences from them are
+                // exact. Vectors that hold infinities have scales that are not
+                // finite: such a token makes the outputs of the rows that see it NaN by
+                // a NaN score, and has finite values, so that the weight 0 of the other rows stays 0.
+                const bool finite = max(szk & 0x7FFFu, szv & 0x7FFFu) < 0x7C00u;
+                const uint32_t sv = finite ? szv & 0x7FFFu : 0u;
                 const float zk = fminf(fmaxf(__half2float(half_hi(szk)), 0.0f), 30.0f);
                 const float zv = fminf(fmaxf(__half2float(half_hi(szv)), 0.0f), 30.0f);
                 sts32(z + 4 * t, half2_bits(__floats2half2_rn(1024.0f + zk, 64.0f + zk)));
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv4_chunk_kernel(const __grid_c
                 const uint32_t f = factors + 4 * ((s & 3) * 2 * kChKeys + t);
                 const uint32_t top = max(max(emax_s[stage][0], emax_s[stage][1]), max(emax_s[stage][2], emax_s[stage][3]));
                 const int ebn = max(eb, (int)(__float_as_uint(half_lo(top)) >> 23));
-                sts32f(f, max(szk & 0xFFFFu, szv & 0xFFFFu) > 0x7BFFu ? __int_as_float(0x7FFFFFFF) : half_lo(szk) * p.qscale);
+                sts32f(f, finite ? half_lo(szk) * p.qscale : __int_as_float(0x7FFFFFFF));
                 sts32f(f + 4 * kChKeys, half_lo(sv) * __int_as_float((262 - ebn) << 23));   // 2^(8 - E)
                 if (t == 0) {
                     es_s[s & 3] = __int_as_float((127 + eb - ebn) << 23);

@@ -443,7 +443,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
         };
         // Whether some row sees token t. What the others hold must not matter: in
         // a tile that is walked for its neighbours they count as zero vectors.
-        auto seen = [&](int t) { return t < r.kv && (pos0 - t < w.reach || t < p.sinks); };
+        const uint32_t hidden = (uint32_t)(p.window ? max(max(pos0 - p.window + 1, 0) - p.sinks, 0) : 0);   // tokens from p.sinks to the first row's window
+        auto seen = [&](int t) { return t < r.kv && (uint32_t)(t - p.sinks) >= hidden; };
         // The scales and zeros of the lane's two tokens, (scale | zero << 16)
         // each; 0 where no row sees them and on bad pages.
         auto load_sz = [&](int k, int pg, uint32_t (&kw)[2], uint32_t (&vw)[2]) {
@@ -460,13 +461,14 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
                 if (in0) kw[0] = kk.x, vw[0] = vv.x;
                 if (in1) kw[1] = kk.y, vw[1] = vv.y;
             } else {
-                // All four at once: they lie in the page, seen or not.
-                const uint32_t k0 = __ldg(reinterpret_cast<const uint32_t *>(at));
-                const uint32_t v0 = __ldg(reinterpret_cast<const uint32_t *>(at + vp_minus_kp));
-                const uint32_t k1 = __ldg(reinterpret_cast<const uint32_t *>(at + 128));
-                const uint32_t v1 = __ldg(reinterpret_cast<const uint32_t *>(at + 128 + vp_minus_kp));
-                if (in0) kw[0] = k0, vw[0] = v0;
-                if (in1) kw[1] = k1, vw[1] = v1;
+                if (in0) {
+                    kw[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+                    vw[0] = __ldg(reinterpret_cast<const uint32_t *>(at + vp_minus_kp));
+                }
+                if (in1) {
+                    kw[1] = __ldg(reinterpret_cast<const uint32_t *>(at + 128));
+                    vw[1] = __ldg(reinterpret_cast<const uint32_t *>(at + 128 + vp_minus_kp));
+                }
             }
         };
 
@@ -581,18 +583,22 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             // Whether every column sees every token of the tile.
             const bool whole = t0 + kRwTile - 1 <= pos0 &&
                                (pos0 + r.n - 1 - t0 < w.reach || t0 + kRwTile <= p.sinks);
-            // The largest value scale (FP16 bits of values >= 0 are ordered),
-            // and the tokens' factors for everyone. A written scale is finite
-            // and a zero at most 22 (15 times the 1.5 by which a subnormal
-            // scale may be rounded down); the bounds, 65504 and 30, make the values'
-            // both finite for whatever a token that some rows do not see may hold,
-            // so that its weight 0 stays 0. A scale that is not finite makes the
-            // score NaN instead, and so the outputs of the rows that see the token.
+            // A written scale is finite, but for vectors that hold infinities. Such a
+            // token makes the outputs of the rows that see it NaN: its score is NaN,
+            // and its value's scale and zero finite, so that the weight 0 of the other rows
+            // stays 0.
+            const uint32_t sk = max(kw[0] & 0x7FFFu, kw[1] & 0x7FFFu);
+            uint32_t sv = max(vw[0] & 0x7FFFu, vw[1] & 0x7FFFu);   // FP16 bits of values >= 0 are ordered
+            const uint32_t zv = max(vw[0] & 0x7FFFFFFFu, vw[1] & 0x7FFFFFFFu);
+            if (__any_sync(0xffffffffu, max(sk, sv) >= 0x7C00u || zv >= 0x7C000000u)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) kw[i] = max(kw[i] & 0xFFFFu, vw[i] & 0xFFFFu) > 0x7BFFu ? 0x7E00u : kw[i];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) vw[i] = min(vw[i] & 0xFFFFu, 0x7BFFu) | (min(vw[i] >> 16, 0x4F80u) << 16);
-            const uint32_t sv = __reduce_max_sync(0xffffffffu, max(vw[0] & 0xFFFFu, vw[1] & 0xFFFFu));
+                for (int i = 0; i < 2; ++i)
+                    if (max(kw[i] & 0x7FFFu, vw[i] & 0x7FFFu) >= 0x7C00u || (vw[i] & 0x7FFFFFFFu) >= 0x7C000000u)
+                        kw[i] = 0x7E00u, vw[i] = 0u;
+                sv = max(vw[0] & 0x7FFFu, vw[1] & 0x7FFFu);
+            }
+            // The tile's largest value scale, and the tokens' factors for everyone.
+            sv = __reduce_max_sync(0xffffffffu, sv);
             const int ebn = max(eb, (int)(__float_as_uint(half_lo(sv)) >> 23));
             const float ef = __int_as_float((262 - ebn) << 23);   // 2^(8 - E)
             __syncwarp();   // every lane is done with the last tile's factors
