@@ -116,16 +116,17 @@ def test_page_steps_of_many_requests(B):
 U = 2.0 ** -24   # the smallest FP16 number, and the step of every scale below 2^-14
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("new", [1, 100])
 @pytest.mark.parametrize("level", [-22, -37, -217, 22])
-def test_values_of_the_smallest_scales(page, new, level):
+def test_values_of_the_smallest_scales(D, page, new, level):
     """Vectors whose scale is subnormal: its rounding makes zeros of up to 22 of
     4-bit codes (-22 units: scale 1, zero 22, code 0)."""
-    b = Batch([90, 0, 300], [new, 3, 1], 8, 2, 128, page, seed=new)
+    b = Batch([90, 0, 300], [new, 3, 1], 8, 2, D, page, seed=new)
     for r in range(3):
         t = np.arange(int(b.kv[r]))
-        x = np.full((len(t), 2, 128), level * U)
+        x = np.full((len(t), 2, D), level * U)
         x[t % 5 == 4] = 3 * U
         put(b, r, t, x, "v")
     if level < 0:
@@ -133,17 +134,18 @@ def test_values_of_the_smallest_scales(page, new, level):
     check(b, run(b))
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("new", [1, 100])
 @pytest.mark.parametrize("level", [-22, -37, -217])
-def test_keys_of_the_smallest_scales(page, new, level):
+def test_keys_of_the_smallest_scales(D, page, new, level):
     """The same among the keys, under queries so large that they count: scores
     0.7 to 4 apart, and values of ordinary size that tell them apart."""
-    b = Batch([90, 0, 300], [new, 3, 1], 8, 2, 128, page, seed=new)
-    b.q[:] = min(50000.0, 4 / (-level * U * np.sqrt(128))) * (0.9 + 0.1 * np.tanh(b.q.astype(np.float64)))
+    b = Batch([90, 0, 300], [new, 3, 1], 8, 2, D, page, seed=new)
+    b.q[:] = min(50000.0, 4 / (-level * U * np.sqrt(D))) * (0.9 + 0.1 * np.tanh(b.q.astype(np.float64)))
     for r in range(3):
         t = np.arange(int(b.kv[r]))
-        x = np.zeros((len(t), 2, 128))
+        x = np.zeros((len(t), 2, D))
         x[t % 3 == 0] = level * U
         put(b, r, t, x, "k")
     check(b, run(b))
@@ -163,13 +165,14 @@ def test_smallest_scales_equal_contiguous_decode():
         check(b, got)
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("gain", [2.0 ** -13, 0.002, 2.0 ** -4])
 @pytest.mark.parametrize("window,sinks", [(50, 2), (1, 0), (1, 1), (130, 20)])
 @pytest.mark.parametrize("bad", [65504.0, np.inf, np.nan])
-def test_scales_of_hidden_tokens_do_not_matter(gain, window, sinks, bad):
+def test_scales_of_hidden_tokens_do_not_matter(D, gain, window, sinks, bad):
     """Tokens that no row sees hold huge, infinite or NaN scales beside small
     visible values: the bound is that of the visible ones alone."""
-    b = Batch([400, 901, 130], [40, 1, 60], 8, 2, 128, 16, seed=9, gain=gain)
+    b = Batch([400, 901, 130], [40, 1, 60], 8, 2, D, 16, seed=9, gain=gain)
     want = b.oracle(window, sinks)
     for r in range(3):
         t = np.arange(sinks, int(b.ctx[r]) - window + 1)
@@ -187,13 +190,14 @@ def _hide(b, window, sinks, number):
                 b.table[r, i] = number
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("window,sinks", [(100, 0), (100, 4), (77, 70), (1, 1)])
 @pytest.mark.parametrize("number", [-1, 10 ** 6])
-def test_pages_without_visible_tokens_may_be_taken_back(page, window, sinks, number):
+def test_pages_without_visible_tokens_may_be_taken_back(D, page, window, sinks, number):
     """Pages between the sinks and the window are no longer in the table:
     no request is refused, the outputs are those of the full table."""
-    b = Batch([1000, 611, 0, 2050, 333], [1, 5, 300, 90, 17], 8, 2, 128, page, seed=page)
+    b = Batch([1000, 611, 0, 2050, 333], [1, 5, 300, 90, 17], 8, 2, D, page, seed=page)
     want = b.oracle(window, sinks)
     _hide(b, window, sinks, number)
     assert (b.table[:, :2] != -1).any()
@@ -246,12 +250,13 @@ def test_queries_of_different_sizes_side_by_side():
     check(b, run(b))
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ctx,new", [([300, 40], [1, 1]), ([5000], [3]), ([200, 0], [100, 70]), ([4000], [60])])
 @pytest.mark.parametrize("what", [np.nan, np.inf])
-def test_queries_that_are_not_numbers(ctx, new, what):
+def test_queries_that_are_not_numbers(D, ctx, new, what):
     """A NaN or infinite component of a query: that row and head's outputs are
     not numbers, the others are as without it."""
-    b = Batch(ctx, new, 8, 2, 128, 64, seed=5)
+    b = Batch(ctx, new, 8, 2, D, 64, seed=5)
     want = b.oracle()
     i, h = b.rows - 1, 5
     b.q[i, h, 17] = what
@@ -262,13 +267,14 @@ def test_queries_that_are_not_numbers(ctx, new, what):
     assert (err <= 2.0 ** -10 * want[1] + 2.0 ** -24).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ctx,new", [([300, 40], [1, 1]), ([5000], [3]), ([200, 0], [100, 70]), ([4000], [60])])
 @pytest.mark.parametrize("tensor", ["k", "v"])
 @pytest.mark.parametrize("what", [np.nan, np.inf])
-def test_visible_scales_that_are_not_numbers(ctx, new, tensor, what):
+def test_visible_scales_that_are_not_numbers(D, ctx, new, tensor, what):
     """A token whose scale is infinite or NaN: the outputs of the rows that see
     it are not numbers, in its KV head alone; rows that do not see it are clean."""
-    b = Batch(ctx, new, 8, 2, 128, 64, seed=7)
+    b = Batch(ctx, new, 8, 2, D, 64, seed=7)
     window, sinks = 90, 3
     want = b.oracle(window, sinks)
     n, kv = int(b.new[0]), int(b.kv[0])
@@ -283,14 +289,15 @@ def test_visible_scales_that_are_not_numbers(ctx, new, tensor, what):
     assert (err[~seen] <= (2.0 ** -10 * want[1] + 2.0 ** -24)[~seen]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ctx,new", [([30], [1]), ([30], [40]), ([3000], [60])])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
-def test_an_infinite_query_under_keys_of_one_sign(ctx, new, sign):
+def test_an_infinite_query_under_keys_of_one_sign(D, ctx, new, sign):
     """Every score of the row is -infinity, or every one +infinity: a softmax of
     either has no value."""
-    b = Batch(ctx, new, 8, 2, 128, 64, seed=8)
+    b = Batch(ctx, new, 8, 2, D, 64, seed=8)
     t = np.arange(int(b.kv[0]))
-    x = np.random.default_rng(8).standard_normal((len(t), 2, 128))
+    x = np.random.default_rng(8).standard_normal((len(t), 2, D))
     x[:, :, 17] = sign * 4
     put(b, 0, t, x, "k")
     want = b.oracle()
@@ -327,16 +334,17 @@ def test_one_workspace_for_calls_of_different_shapes():
             assert np.array_equal(got.view(np.uint16), run(b).view(np.uint16))
 
 
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ctx,new", [([300, 40], [1, 1]), ([200, 0], [100, 70])])
-def test_negative_zeros_among_the_parameters(ctx, new):
+def test_negative_zeros_among_the_parameters(D, ctx, new):
     """A cache filled by other means may hold -0 as a zero or a scale: 0."""
-    b = Batch(ctx, new, 8, 2, 128, 64, seed=2)
+    b = Batch(ctx, new, 8, 2, D, 64, seed=2)
     rng = np.random.default_rng(2)
     for r in range(2):
         t = np.arange(int(b.kv[r]))
         for name in "kv":
-            put(b, r, t, np.abs(rng.standard_normal((len(t), 2, 128))), name)
-            put(b, r, t[::5], np.zeros((len(t[::5]), 2, 128)), name)
+            put(b, r, t, np.abs(rng.standard_normal((len(t), 2, D))), name)
+            put(b, r, t[::5], np.zeros((len(t[::5]), 2, D)), name)
     want = b.oracle()
     for params in (b.k_params, b.v_params):
         params[params == 0] = np.float16(-0.0)

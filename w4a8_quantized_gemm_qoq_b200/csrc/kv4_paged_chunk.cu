@@ -311,7 +311,6 @@ __device__ __forceinline__ void mma4_f16_ts(uint32_t d, uint32_t a, uint32_t b, 
         : "memory");
 }
 
-// Two FP32 values in one register pair, each operation on both.
 // The accesses below are warp-collective: the warp must be converged.
 //
 // Loads of 16 lanes x 32 columns in the layout of matrix fragments: lane t's
@@ -615,7 +614,9 @@ __device__ __forceinline__ void softmax_rows(uint32_t ts, uint32_t kf, uint32_t 
                     b.x[i >> 1][2 * j + (i & 1)] = add2(b.x[i >> 1][2 * j + (i & 1)], pair_of(-up, -up));
             }
             __syncwarp();
-            // The step's weights stored so far. A load of tensor memory is ordered
+            // The step's weights stored so far, times a power of two: exact, but for those
+            // that become subnormal, which are rounded a second time, by at most 2^-25
+            // beside a largest weight of some 2^8. A load of tensor memory is ordered
             // behind this warp's own stores of it by their wait alone.
             if (q > 0) tmem_st_wait();
 #pragma unroll 1
