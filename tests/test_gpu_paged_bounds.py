@@ -349,3 +349,23 @@ def test_negative_zeros_among_the_parameters(D, ctx, new):
     for params in (b.k_params, b.v_params):
         params[params == 0] = np.float16(-0.0)
     check(b, run(b), want=want)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_the_largest_batch(many):
+    """16384 requests, the most a step takes, with and without requests of many rows."""
+    rng = np.random.default_rng(1)
+    new = rng.integers(0, 3, 16384)
+    if many:
+        new[::3000] = 40
+    b = Batch(rng.integers(0, 20, 16384), new, 2, 1, 64, 16, seed=1, spare_rows=1)
+    check(b, run(b))
+
+
+@pytest.mark.parametrize("B", [1, 7, 130, 2100])
+def test_a_step_without_rows(B):
+    """No request brings a token: nothing is written, nothing refused."""
+    b = Batch([30] * B, [0] * B, 8, 2, 64, 16, seed=1, spare_rows=60)
+    run(b, max_new=1)
+    run(b, max_new=60)
+    run(b, 7, 1, max_new=60)
