@@ -11,15 +11,20 @@ size_t kv4_paged_workspace_bytes(int64_t B, int64_t, int64_t Hq, int64_t Hkv, in
 }
 
 // A request with at most 48 (row, head) pairs per KV head goes to the few-rows
-// kernel, the others to the many-rows one. Measured on both sides of it, 32 sequences
-// of 1500 to 4500 tokens, 8 KV heads of 128: with 8, 16, 24, 32, 40, 48 and 64
-// pairs the former takes 34, 52, 70, 86, 104, 122 and 157 us, the latter
-// 127 to 132 us with 16 to 64 of them. Which requests have few rows is known on the
-// device only: N and max_new are what the buffers have room for. So where
-// some may have many, both kernels run. Where all of them do, the few-rows kernel
-// finds nothing, which costs 1 to 2 us (a prompt of 100 in 20.4 us, of 4096 in 234.2, without
-// it 19.4 and 232.0); without it 32 decoding requests in a step with room for
-// 16 rows each take 121 us, not 38.7, and 5 drafted tokens of each 126, not 76.
+// kernel, the others to the many-rows one. Both sides of it, in us with 16, 32, 48, 56 and 64
+// pairs (8 KV heads), few-rows kernel / many-rows kernel:
+//   32 sequences of 1500 to 4500 tokens, D 128   49/134  82/137  118/141  137/141  153/138
+//   the same, D 64                               33/116  54/118   78/120   88/120  100/123
+//   one of 16000 tokens, D 128                   20/46   26/47    32/48    35/49    38/50
+//   4 of 2000 tokens, D 128                      15/31   19/32    23/33    23/33    26/34
+// In the first, the heaviest, the sides meet at 56 pairs; in the others later.
+//
+// Which requests have few rows is known on the device only: N and max_new are
+// what the buffers have room for. So where some may have many, both kernels run.
+// Where all of them do, the few-rows kernel finds nothing, which costs 1 to 2 us (a
+// prompt of 100 tokens in 20.3 us, of 4096 in 234.3; 19.2 and 232.0 without it).
+// Where they do not, as in a captured step with room for 16 rows of each of 32 requests, a
+// decode step takes 38.7 us and not 121, 5 drafted tokens of each 76 and not 126.
 cudaError_t launch_paged_attention(const PagedAttnParams &p, int64_t D, int64_t max_new, void *ws,
                                    cudaStream_t stream) {
     uint8_t *at = static_cast<uint8_t *>(ws) + 256;

@@ -24,9 +24,9 @@
 //
 // Per 128 keys and 256 rows the tensor core needs 2048 cycles and so does
 // the exponential unit (16 a cycle and SM): the two would bound the kernel
-// together. Measured (32 query heads on 8, D 128): 2048 rows on 16384 tokens 723 us
-// (713 TFLOP/s of 1614 that a large product reaches), a prompt of 4096 231 us
-// (593). A step of 128 keys takes some 6800 cycles: a softmax 2400 alone and
+// together. Measured (32 query heads on 8, D 128): 2048 rows on 16384 tokens 727 us
+// (709 TFLOP/s of 1614 that a large product reaches), a prompt of 4096 235 us
+// (584). A step of 128 keys takes some 6800 cycles: a softmax 2400 alone and
 // 4000 beside the other one, then about 1900 until the products of its row tile are
 // through, since tensor memory holds two outputs and two score tiles and no third (P
 // lies over S, so the next scores wait for this step's second product).
@@ -36,7 +36,7 @@
 // last block's weights (912, for want of registers), blocks of 16 keys (909) or
 // votes on 64 (759), softmaxes made to take turns (836), weights handed over by
 // halves of a step (778; by polling for whichever tile is ready 825), two unpacking
-// warpgroups (771 when that was tried against 748).
+// warpgroups (771 when that was tried against 748); the others were tried against 723 to 728.
 //
 // Pieces: (request, KV head, 256-row tile) items, long ones first, each cut
 // along the keys into equal parts when there are too few of them to fill the
@@ -64,7 +64,7 @@ constexpr int kChSlots = 2 * kChCtas;   // pieces of divided items
 constexpr int kChOverhead = 3;       // cost of a piece beside its steps, in steps
 // Registers per thread: the pool is 512 threads x 128, of which the roles take
 // 256 x 176 + 128 x 104 + 128 x 56 = 65536 (184 / 104 / 40 spills in the issuing
-// warp: 727 us for the first case above, not 723).
+// warp: 727 us for the first case above where this split took 723).
 constexpr int kRegsSoftmax = 176, kRegsUnpack = 104, kRegsIssue = 56;
 constexpr float kChSlack = 6.0f;     // log2 by which scores may exceed the running maximum
 constexpr int kDvThreads = 1024;

@@ -9,12 +9,11 @@
 // the same cache again (from L2, as they run side by side).
 //
 // Measured (8 KV heads of 128, 4 query heads each, GPU time of a call): 64
-// sequences of 1024 tokens in 23.5 us (3.1 TB/s), of 4096 in 68 us (4.2 TB/s),
-// 74 of 4096, which fill the GPU evenly, in 73 us (4.5 TB/s of 6.6 that a copy
-// reaches); one of 64 tokens in 6.5 us. At length a round (64 tokens in
-// each of 16 warps per SM) takes 4 us for some 15000 issued instructions: two
-// per cycle, the ALU pipe 55% busy with unpacking, so that neither bytes nor
-// one pipe but the mix of issue slots and latencies of 16 warps bounds it.
+// sequences of 1024 tokens in 23.1 us (3.1 TB/s), of 4096 in 62 us (4.6 TB/s),
+// 74 of 4096, which fill the GPU evenly, in 63 us (5.2 TB/s of 6.6 that a copy
+// reaches); one of 64 tokens in 5.8 us. At length the issue slots are 55% taken, the
+// ALU pipe, which unpacks, 55%, the tensor pipe 31% and the memory 60%: none at its
+// limit, and four warps per scheduler (of 128 registers each) wait for their own chains.
 //
 // The division. The lengths are known on the device only, so every CTA works out
 // the same division: a request's visible tokens are 64-token tiles (those of
@@ -22,7 +21,7 @@
 // all items, one after another, are cut into equal shares, one per resident CTA
 // (four per SM), so that all SMs end together whatever the mix of lengths (24
 // sequences of 100 to 32700 tokens in pages of 16 took 52 us when this was
-// introduced, 56 in even pieces of each item; 46 now). An item that several
+// introduced, 56 in even pieces of each item; 46.4 now). An item that several
 // CTAs share leaves FP32 partial sums, which the last to arrive combines in a
 // fixed order.
 //
@@ -38,8 +37,8 @@
 // in a half's low nibble, c * 2^-20 in the next one, one AND per two codes and
 // one shift per four), transposed loads of 16-bit units pair the value codes
 // of neighbouring tokens without byte permutes, the queries that meet high
-// nibbles are divided by 16 beforehand so that one accumulator takes both,
-// and the zero points are subtracted afterwards: s (q.c) - s z sum(q) per
+// nibbles are divided by 16 beforehand, after a scaling that keeps their bits, so
+// that one accumulator takes both, and the zero points are subtracted afterwards: s (q.c) - s z sum(q) per
 // score in FP32, and for the values as one more product row, sum_t P_t z_t.
 // Token factors are converted once per token and read back by broadcast.
 //
