@@ -441,8 +441,10 @@ __global__ void __launch_bounds__(kRwThreads, 4) kv4_rows_kernel(const __grid_co
             copy_commit();
         };
         // Whether some row sees token t. What the others hold must not matter: in
-        // a tile that is walked for its neighbours they count as zero vectors.
-        const uint32_t hidden = (uint32_t)(p.window ? max(max(pos0 - p.window + 1, 0) - p.sinks, 0) : 0);   // tokens from p.sinks to the first row's window
+        // a tile that is walked for its neighbours they count as zero vectors. They
+        // are the `hidden` tokens from p.sinks to the first row's window. A branch
+        // skips their loads (loaded and then dropped they cost 3%).
+        const uint32_t hidden = (uint32_t)(p.window ? max(max(pos0 - p.window + 1, 0) - p.sinks, 0) : 0);
         auto seen = [&](int t) { return t < r.kv && (uint32_t)(t - p.sinks) >= hidden; };
         // The scales and zeros of the lane's two tokens, (scale | zero << 16)
         // each; 0 where no row sees them and on bad pages.
